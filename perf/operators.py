@@ -149,8 +149,8 @@ def prepare(case, seed):
         state["w"] = _weight(g, E, case["N"], case["K"])
         state["bias"] = _bias(g, (E, case["N"]), dtype, case["bias"])
     else:
-        # up: rows 0..I-1 the gate, rows I..2I-1 the other factor
-        state["up"] = _weight(g, E, 2 * case["I"], case["K"])
+        # up: two matrices [I, K] per expert, the gate and the other factor
+        state["up"] = _weight(g, 2 * E, case["I"], case["K"])
         state["down"] = _weight(g, E, case["K"], case["I"])
         state["up_bias"] = _bias(g, (E, 2 * case["I"]), dtype, case["bias"])
         state["down_bias"] = _bias(g, (E, case["K"]), dtype, case["bias"])
@@ -198,11 +198,13 @@ def _plain_groups(state):
     return expert, row - off[expert]
 
 
-def _plain_experts(x, w, expert, place, most, bias):
-    """Each row of x [R, K] (32 bits) times its own expert's weight."""
-    padded = x.new_zeros(w["E"], most, x.shape[1])
+def _plain_experts(x, w, E, expert, place, most, bias):
+    """Each row of x [R, K] (32 bits) times its own expert's weight (all the
+    matrices of an expert one below the other)."""
+    padded = x.new_zeros(E, most, x.shape[1])
     padded[expert, place] = _plain_rounded(x)
-    y = torch.bmm(padded, _plain_values(w["codes"], w["rowmajor"]).transpose(1, 2))[expert, place]
+    values = _plain_values(w["codes"], w["rowmajor"]).view(E, -1, x.shape[1])
+    y = torch.bmm(padded, values.transpose(1, 2))[expert, place]
     return y if bias is None else y + bias.float()[expert]
 
 
@@ -217,13 +219,15 @@ def _plain(state):
         y = y if state["bias"] is None else y + state["bias"].float()
         return {"y": y.to(state["dtype"])}
     expert, place = _plain_groups(state)
+    E = state["offsets"].numel() - 1
     x = state["x"].float() if state["row_index"] is None else state["x"].float()[state["row_index"].long()]
     if op == "grouped":
-        y = _plain_experts(x, state["w"], expert, place, state["most"], state["bias"])
+        y = _plain_experts(x, state["w"], E, expert, place, state["most"], state["bias"])
         return {"y": y.to(state["dtype"])}
-    gate, other = _plain_experts(x, state["up"], expert, place, state["most"], state["up_bias"]).chunk(2, 1)
+    both = _plain_experts(x, state["up"], E, expert, place, state["most"], state["up_bias"])
+    gate, other = both.chunk(2, 1)
     h = gate / (1.0 + torch.exp(-gate)) * other
-    y = _plain_experts(h, state["down"], expert, place, state["most"], state["down_bias"])
+    y = _plain_experts(h, state["down"], E, expert, place, state["most"], state["down_bias"])
     return {"y": y.to(state["dtype"])}
 
 
@@ -317,7 +321,8 @@ def exact(case, seed):
     off = state["offsets"].tolist()
 
     def expert_product(h, w, bias, e):
-        y = _exact_values64(h) @ _exact_weight64(w["codes"][e], w["rowmajor"][e]).t()
+        codes, scales = (w[k].view(case["E"], -1, w[k].shape[-1])[e] for k in ("codes", "rowmajor"))
+        y = _exact_values64(h) @ _exact_weight64(codes, scales).t()
         return y if bias is None else y + bias[e].double()
 
     parts = []
