@@ -65,6 +65,21 @@ def _load():
         "svdq_w4a4_linear_noalloc": (I, [I, I, I, I, I, P, P, P, F, P, P, F, P, P, P, P, P]),
         "awq_pack_weights": (I, [I, I, P, P, P, P]),
         "awq_w4a16_linear": (I, [I, I, I, P, P, P, P, P, P, P]),
+        "mxfp4_scale_bytes": (LL, [I, I]),
+        "mxfp4_grouped_scale_bytes": (LL, [I, I, I]),
+        "mxfp4_workspace_bytes": (LL, [I, I, I]),
+        "mxfp4_mlp_workspace_bytes": (LL, [I, I, I, I]),
+        "mxfp4_pack_weights": (I, [I, I, I, P, P, P]),
+        "mxfp4_scales_to_rowmajor": (I, [I, I, I, P, P]),
+        "mxfp4_scales_from_rowmajor": (I, [I, I, I, P, P]),
+        "mxfp4_quantize": (I, [I, I, I, P, LL, P, I, I, P, P, P, P, P]),
+        "mxfp4_dequantize": (I, [I, I, I, P, P, I, P, P, LL, P, P]),
+        "mxfp4_gemm": (I, [I, I, I, I, P, P, P, P, P, P, LL, P, P]),
+        "mxfp4_grouped_gemm": (I, [I, I, I, I, I, P, P, P, P, P, P, P, LL, P, P]),
+        "mxfp4_linear": (I, [I, I, I, I, P, LL, P, P, P, P, LL, P, LL, P, P]),
+        "mxfp4_grouped_linear": (I, [I, I, I, I, I, P, LL, P, I, P, P, P, P, P, LL, P, LL, P, P]),
+        "mxfp4_grouped_gemm_swiglu_quant": (I, [I, I, I, I, I, P, P, P, P, P, P, P, P, P, P]),
+        "mxfp4_grouped_mlp_swiglu": (I, [I, I, I, I, I, P, LL, P, I, P, P, P, P, P, P, P, P, LL, P, LL, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -422,4 +437,300 @@ def awq_w4a16_linear(x, w, bias=None, y=None, stream=None):
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     _check(lib.awq_w4a16_linear(M, N, K, _ptr(x), _ptr(w["qweight"]), _ptr(w["scales"]), _ptr(w["zeros"]),
                                 _ptr(bias), _ptr(y), _stream(stream)))
+    return y
+
+
+# ------------------------------------------------------------------ MXFP4
+
+MXFP4_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+MXFP4_MAX_GROUPS = 512
+
+
+def mxfp4_scale_bytes(rows, K, groups=0):
+    """Bytes of the tiled E8M0 scales of [rows, K]; with ``groups`` those of
+    the grouped layout."""
+    return int(lib.mxfp4_grouped_scale_bytes(groups, rows, K) if groups else lib.mxfp4_scale_bytes(rows, K))
+
+
+def mxfp4_workspace_bytes(rows, K, groups=0):
+    return int(lib.mxfp4_workspace_bytes(groups, rows, K))
+
+
+def mxfp4_mlp_workspace_bytes(groups, rows, K, I):
+    return int(lib.mxfp4_mlp_workspace_bytes(groups, rows, K, I))
+
+
+def mxfp4_pack_weights(W_bits):
+    """Host pack of bf16 weights (uint16 bit patterns) [N, K], or several
+    [..., N, K]: a dict of host arrays, moved with ``to_device``.  The up
+    weight of ``mxfp4_grouped_mlp_swiglu`` is [E, 2, I, K]: per expert the
+    gate's matrix, then the other factor's."""
+    W_bits = np.ascontiguousarray(W_bits, dtype=np.uint16)
+    N, K = W_bits.shape[-2:]
+    lead = W_bits.shape[:-2]
+    E = int(np.prod(lead)) if lead else 1
+    size = mxfp4_scale_bytes(N, K)
+    if size < 0:
+        raise SvdqError(2, f"unsupported shape N={N} K={K}")
+    out = {"codes": np.empty(lead + (N, K // 2), np.uint8), "scales": np.empty(lead + (size,), np.uint8)}
+    _check(lib.mxfp4_pack_weights(E, N, K, _ptr(W_bits), _ptr(out["codes"]), _ptr(out["scales"])))
+    out["N"], out["K"], out["E"] = N, K, E
+    return out
+
+
+def mxfp4_scales_to_rowmajor(tiled, rows, K):
+    """Tiled scales of [..., rows, K] (uint8 [..., mxfp4_scale_bytes]) -> uint8 [..., rows, K/32]."""
+    tiled = np.ascontiguousarray(np.asarray(tiled, dtype=np.uint8))
+    lead = tiled.shape[:-1]
+    if tiled.shape[-1] != mxfp4_scale_bytes(rows, K):
+        raise SvdqError(2, f"{tiled.shape[-1]} scale bytes do not match [{rows}, {K}]")
+    out = np.empty(lead + (rows, K // 32), np.uint8)
+    _check(lib.mxfp4_scales_to_rowmajor(int(np.prod(lead)) if lead else 1, rows, K, _ptr(tiled), _ptr(out)))
+    return out
+
+
+def mxfp4_scales_from_rowmajor(rowmajor):
+    """Scales uint8 [..., rows, K/32], as checkpoints hold them -> tiled uint8 [..., mxfp4_scale_bytes]."""
+    rowmajor = np.ascontiguousarray(np.asarray(rowmajor, dtype=np.uint8))
+    rows, K = rowmajor.shape[-2], rowmajor.shape[-1] * 32
+    lead = rowmajor.shape[:-2]
+    out = np.empty(lead + (max(mxfp4_scale_bytes(rows, K), 0),), np.uint8)
+    _check(lib.mxfp4_scales_from_rowmajor(int(np.prod(lead)) if lead else 1, rows, K, _ptr(rowmajor), _ptr(out)))
+    return out
+
+
+def _mx_call(device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current, on its current
+    stream unless one is given."""
+    if device.index == torch.cuda.current_device():
+        return _check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)))
+    with torch.cuda.device(device):
+        return _check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)))
+
+
+def _mx_rows(t, name, dtypes):
+    """(mxfp4 dtype, row stride) of a CUDA matrix whose rows are contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2):
+        raise TypeError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return MXFP4_DTYPES[t.dtype], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _mx_like(t, name, device, dtype, count):
+    """Data pointer of a contiguous tensor of ``count`` elements, or of None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device):
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
+    if not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{name} must be contiguous and have {count} elements (it has {t.numel()})")
+    return t.data_ptr()
+
+
+def _mx_weight(w, name, device, N, K, matrices):
+    if w["N"] != N or w["K"] != K or w.get("E", 1) != matrices:
+        raise SvdqError(2, f"{name} is {w.get('E', 1)} x [{w['N']}, {w['K']}], not {matrices} x [{N}, {K}]")
+    return (_mx_like(w["codes"], name + " codes", device, torch.uint8, matrices * N * (K // 2)),
+            _mx_like(w["scales"], name + " scales", device, torch.uint8, matrices * mxfp4_scale_bytes(N, K)))
+
+
+def _mx_groups(offsets, device):
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise TypeError("offsets must be an int32 tensor [groups + 1]")
+    return offsets.numel() - 1, _mx_like(offsets, "offsets", device, torch.int32, offsets.numel())
+
+
+def _mx_out(y, rows, N, dtype, device):
+    if y is None:
+        return torch.empty((rows, N), dtype=dtype, device=device), N
+    _, ldy = _mx_rows(y, "y", (dtype,))
+    if y.shape != (rows, N) or y.device != device:
+        raise ValueError(f"y must be [{rows}, {N}] on {device}")
+    return y, ldy
+
+
+def _mx_workspace(workspace, need, device):
+    if need < 0:
+        raise SvdqError(2, "unsupported shape")
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise TypeError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def _mx_status(dev_status, device):
+    return _mx_like(dev_status, "dev_status", device, torch.int32, 1)
+
+
+_MX_INPUT = (torch.bfloat16, torch.float16, torch.float32)
+_MX_LAYER = (torch.bfloat16, torch.float16)
+
+
+def mxfp4_quantize(x, offsets=None, row_index=None, out=None, dev_status=None, stream=None):
+    """Rows of x (bf16, fp16 or fp32 [T, K]) -> (codes uint8 [rows, K/2],
+    tiled E8M0 scales uint8).  ``row_index`` (int32 [rows]): row i is
+    x[row_index[i]].  ``offsets`` (int32 [groups + 1]): scales in the grouped
+    layout; rows of no group are skipped."""
+    dtype, ldx = _mx_rows(x, "x", _MX_INPUT)
+    dev = x.device
+    x_rows, K = x.shape
+    rows = x_rows if row_index is None else row_index.numel()
+    groups, off = (0, None) if offsets is None else _mx_groups(offsets, dev)
+    size = mxfp4_scale_bytes(rows, K, groups)
+    if size < 0:
+        raise SvdqError(2, f"unsupported shape rows={rows} K={K} groups={groups}")
+    if out is None:
+        out = (torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
+               torch.empty(size, dtype=torch.uint8, device=dev))
+    codes, scales = out
+    _mx_call(dev, stream, lib.mxfp4_quantize, dtype, rows, K, x.data_ptr(), ldx,
+             _mx_like(row_index, "row_index", dev, torch.int32, rows), x_rows, groups, off,
+             _mx_like(codes, "codes", dev, torch.uint8, rows * (K // 2)),
+             _mx_like(scales, "scales", dev, torch.uint8, size), _mx_status(dev_status, dev))
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, offsets=None, dtype=torch.bfloat16, out=None, dev_status=None, stream=None):
+    """The values (bf16 or fp32 [rows, K]) that codes and scales stand for;
+    with ``offsets`` rows of no group are left as they were (0 in a new
+    output)."""
+    if not (isinstance(codes, torch.Tensor) and codes.is_cuda and codes.dtype == torch.uint8 and codes.dim() == 2):
+        raise TypeError("codes must be a 2-D CUDA uint8 tensor")
+    dev = codes.device
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    groups, off = (0, None) if offsets is None else _mx_groups(offsets, dev)
+    if out is None:
+        out = (torch.empty if offsets is None else torch.zeros)((rows, K), dtype=dtype, device=dev)
+    out, ldo = _mx_out(out, rows, K, dtype, dev)
+    size = mxfp4_scale_bytes(rows, K, groups)
+    if size < 0 or dtype not in (torch.bfloat16, torch.float32):
+        raise SvdqError(2, f"unsupported shape or dtype: rows={rows} K={K} groups={groups} {dtype}")
+    _mx_call(dev, stream, lib.mxfp4_dequantize, MXFP4_DTYPES[dtype], rows, K,
+             _mx_like(codes, "codes", dev, torch.uint8, rows * (K // 2)),
+             _mx_like(scales, "scales", dev, torch.uint8, size), groups, off, out.data_ptr(), ldo,
+             _mx_status(dev_status, dev))
+    return out
+
+
+def mxfp4_gemm(codes, scales, w, bias=None, dtype=torch.bfloat16, y=None, dev_status=None, stream=None):
+    """y [M, N] (bf16 or fp16) of quantized rows and a weight: a device dict
+    from to_device(mxfp4_pack_weights(...)), or any with "codes", "scales",
+    "N" and "K"."""
+    return _mx_gemm(codes, scales, None, w, bias, dtype, y, dev_status, stream)
+
+
+def mxfp4_grouped_gemm(codes, scales, offsets, w, bias=None, dtype=torch.bfloat16, y=None, dev_status=None,
+                       stream=None):
+    """mxfp4_gemm per row group: rows offsets[e] .. offsets[e + 1] - 1 with
+    weight e ("E" matrices).  Rows of no group are left as they were (not
+    initialized in a new output)."""
+    return _mx_gemm(codes, scales, offsets, w, bias, dtype, y, dev_status, stream)
+
+
+def _mx_gemm(codes, scales, offsets, w, bias, dtype, y, dev_status, stream):
+    if not (isinstance(codes, torch.Tensor) and codes.is_cuda and codes.dtype == torch.uint8 and codes.dim() == 2):
+        raise TypeError("codes must be a 2-D CUDA uint8 tensor")
+    if dtype not in _MX_LAYER:
+        raise TypeError("dtype must be torch.bfloat16 or torch.float16")
+    dev = codes.device
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    N = w["N"]
+    groups, off = (0, None) if offsets is None else _mx_groups(offsets, dev)
+    wc, ws = _mx_weight(w, "w", dev, N, K, groups or 1)
+    y, ldy = _mx_out(y, rows, N, dtype, dev)
+    _mx_call(dev, stream, lib.mxfp4_grouped_gemm, MXFP4_DTYPES[dtype], groups, rows, N, K, off,
+             _mx_like(codes, "codes", dev, torch.uint8, rows * (K // 2)),
+             _mx_like(scales, "scales", dev, torch.uint8, mxfp4_scale_bytes(rows, K, groups)), wc, ws,
+             _mx_like(bias, "bias", dev, dtype, (groups or 1) * N), y.data_ptr(), ldy, _mx_status(dev_status, dev))
+    return y
+
+
+def mxfp4_linear(x, w, bias=None, y=None, workspace=None, dev_status=None, stream=None):
+    """y = Q(x) deq(W)^T + bias for x bf16 or fp16 [M, K]; y has x's type."""
+    dtype, ldx = _mx_rows(x, "x", _MX_LAYER)
+    dev = x.device
+    M, K = x.shape
+    N = w["N"]
+    wc, ws = _mx_weight(w, "w", dev, N, K, 1)
+    y, ldy = _mx_out(y, M, N, x.dtype, dev)
+    workspace = _mx_workspace(workspace, mxfp4_workspace_bytes(M, K), dev)
+    _mx_call(dev, stream, lib.mxfp4_linear, dtype, M, N, K, x.data_ptr(), ldx, wc, ws,
+             _mx_like(bias, "bias", dev, x.dtype, N), y.data_ptr(), ldy, workspace.data_ptr(), workspace.numel(),
+             _mx_status(dev_status, dev))
+    return y
+
+
+def mxfp4_grouped_linear(x, offsets, w, row_index=None, bias=None, y=None, workspace=None, dev_status=None,
+                         stream=None):
+    """mxfp4_linear per row group: row i of y [rows, N] is row i of x, or
+    x[row_index[i]], times the weight of the group that owns row i."""
+    dtype, ldx = _mx_rows(x, "x", _MX_LAYER)
+    dev = x.device
+    x_rows, K = x.shape
+    rows = x_rows if row_index is None else row_index.numel()
+    N = w["N"]
+    groups, off = _mx_groups(offsets, dev)
+    wc, ws = _mx_weight(w, "w", dev, N, K, groups)
+    y, ldy = _mx_out(y, rows, N, x.dtype, dev)
+    workspace = _mx_workspace(workspace, mxfp4_workspace_bytes(rows, K, groups), dev)
+    _mx_call(dev, stream, lib.mxfp4_grouped_linear, dtype, groups, rows, N, K, x.data_ptr(), ldx,
+             _mx_like(row_index, "row_index", dev, torch.int32, rows), x_rows, off, wc, ws,
+             _mx_like(bias, "bias", dev, x.dtype, groups * N), y.data_ptr(), ldy, workspace.data_ptr(),
+             workspace.numel(), _mx_status(dev_status, dev))
+    return y
+
+
+def mxfp4_grouped_gemm_swiglu_quant(codes, scales, offsets, w, bias=None, dtype=torch.bfloat16, out=None,
+                                    dev_status=None, stream=None):
+    """The experts' up product with SwiGLU and requantization in its
+    epilogue: w holds two matrices [I, K] per group (gate, other), bias
+    [groups, 2, I] of ``dtype``.  Returns (codes [rows, I/2], grouped scales)
+    of h = g sigmoid(g) u."""
+    if not (isinstance(codes, torch.Tensor) and codes.is_cuda and codes.dtype == torch.uint8 and codes.dim() == 2):
+        raise TypeError("codes must be a 2-D CUDA uint8 tensor")
+    if dtype not in _MX_LAYER:
+        raise TypeError("dtype must be torch.bfloat16 or torch.float16")
+    dev = codes.device
+    rows, K = codes.shape[0], codes.shape[1] * 2
+    width = w["N"]
+    groups, off = _mx_groups(offsets, dev)
+    wc, ws = _mx_weight(w, "w", dev, width, K, 2 * groups)
+    size = mxfp4_scale_bytes(rows, width, groups)
+    if size < 0:
+        raise SvdqError(2, f"unsupported shape rows={rows} I={width} groups={groups}")
+    if out is None:
+        out = (torch.empty((rows, width // 2), dtype=torch.uint8, device=dev),
+               torch.empty(size, dtype=torch.uint8, device=dev))
+    h_codes, h_scales = out
+    _mx_call(dev, stream, lib.mxfp4_grouped_gemm_swiglu_quant, MXFP4_DTYPES[dtype], groups, rows, width, K, off,
+             _mx_like(codes, "codes", dev, torch.uint8, rows * (K // 2)),
+             _mx_like(scales, "scales", dev, torch.uint8, mxfp4_scale_bytes(rows, K, groups)), wc, ws,
+             _mx_like(bias, "bias", dev, dtype, 2 * groups * width),
+             _mx_like(h_codes, "out codes", dev, torch.uint8, rows * (width // 2)),
+             _mx_like(h_scales, "out scales", dev, torch.uint8, size), _mx_status(dev_status, dev))
+    return h_codes, h_scales
+
+
+def mxfp4_grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index=None, up_bias=None, down_bias=None, y=None,
+                             workspace=None, dev_status=None, stream=None):
+    """The experts' MLP y = down(SwiGLU(up(x))) per row group: w_up two
+    matrices [I, K] per group (gate, other), w_down [groups, K, I]; the hidden
+    rows are quantized in the up product's epilogue."""
+    dtype, ldx = _mx_rows(x, "x", _MX_LAYER)
+    dev = x.device
+    x_rows, K = x.shape
+    rows = x_rows if row_index is None else row_index.numel()
+    width = w_up["N"]
+    groups, off = _mx_groups(offsets, dev)
+    uc, us = _mx_weight(w_up, "w_up", dev, width, K, 2 * groups)
+    dc, ds = _mx_weight(w_down, "w_down", dev, K, width, groups)
+    y, ldy = _mx_out(y, rows, K, x.dtype, dev)
+    workspace = _mx_workspace(workspace, mxfp4_mlp_workspace_bytes(groups, rows, K, width), dev)
+    _mx_call(dev, stream, lib.mxfp4_grouped_mlp_swiglu, dtype, groups, rows, K, width, x.data_ptr(), ldx,
+             _mx_like(row_index, "row_index", dev, torch.int32, rows), x_rows, off, uc, us,
+             _mx_like(up_bias, "up_bias", dev, x.dtype, 2 * groups * width), dc, ds,
+             _mx_like(down_bias, "down_bias", dev, x.dtype, groups * K), y.data_ptr(), ldy, workspace.data_ptr(),
+             workspace.numel(), _mx_status(dev_status, dev))
     return y

@@ -161,6 +161,10 @@ int record_error(int status, const char* fmt, ...) {
   return status;
 }
 
+int require_device(int* sms) { return check_device(sms); }
+int status_word(int** dev_status) { return resolve_status(dev_status); }
+bool pdl_enabled() { return pdl_on(); }
+
 unsigned long long current_context_id() {
   using CtxGetCurrentFn = CUresult (*)(CUcontext*);
   using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long*);

@@ -1,0 +1,189 @@
+// Shared pieces of the MXFP4 kernels: the scale layout, the block scale and
+// element encodings, the list of row groups and the tile schedule over it.
+//
+// MXFP4 (OCP Microscaling Formats v1.0): E2M1 elements in blocks of 32 along
+// K that share an E8M0 scale, one byte b standing for 2^(b - 127); 0xFF is
+// NaN.  A block with t = max|v| gets the scale 2^max(floor(log2 t) - 2, -127)
+// (section 6.3: the exponent of t less that of E2M1's largest power of two),
+// and its elements v / scale round to the nearest E2M1 value, ties to even,
+// at most 6 in magnitude.  A block that holds a NaN or an infinity gets 0xFF
+// and zero codes, so that every product with it is NaN.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "svdq_internal.h"
+
+namespace svdq {
+
+// ------------------------------------------------------------------ encoding
+// Scale byte of a block from the bits of max|v| (fp32, sign cleared; compared
+// as integers, so that NaN and infinity win).
+SVDQ_DEV uint32_t mx_scale_byte(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+// 1 / scale, exact: the byte is at most 252, so 2^(127 - b) is normal.  Zero
+// for the NaN byte, which makes every code of such a block zero.
+SVDQ_DEV float mx_inv_scale(uint32_t byte) { return byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23); }
+
+// Eight fp32 -> four bytes of E2M1 codes, element 2i in bits 8i..8i+3 and
+// element 2i+1 in bits 8i+4..8i+7; RNE, satfinite.
+SVDQ_DEV uint32_t mx_e2m1x8(const float (&v)[8]) {
+  uint32_t out;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(out)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return out;
+}
+
+// ------------------------------------------------------------------ layout
+// Scales: 512-byte tiles of 128 rows x 4 blocks (128 elements of K), the
+// tiles of one 128-row block next to each other: byte (row r of the block,
+// group g) at (g / 4) * 512 + (r % 32) * 16 + (r / 32) * 4 + g % 4.  Rows of a
+// block past the last and groups past K / 32 are padding.
+SVDQ_DEV size_t mx_tile_offset(int block, int k_chunks, int chunk) {
+  return ((size_t)block * k_chunks + chunk) * 512;
+}
+
+// Row groups: group e owns rows [offsets[e], offsets[e + 1]).  Its scale
+// blocks begin at block offsets[e] / 128 + e: since
+// floor((a + c) / 128) - floor(a / 128) + 1 >= ceil(c / 128), a group's blocks
+// never reach the next group's, and no prefix sum is needed to find them.
+SVDQ_DEV int mx_first_block(int offset, int e) { return (offset >> 7) + e; }
+
+// ------------------------------------------------------------------ schedule
+// Tiles of a grouped product, in shared memory: the groups' first rows and
+// the running count of their row tiles.
+struct MxSched {
+  int off[kMxMaxGroups + 1];
+  int pre[kMxMaxGroups + 1];
+};
+
+// Filled by one whole warp.  Offsets that decrease or leave [0, rows] give an
+// empty schedule and a status code.
+SVDQ_DEV void mx_build_sched(MxSched* s, int groups, const int* offsets, int rows, int tile_rows, int* dev_status) {
+  const int lane = threadIdx.x & 31;
+  if (groups == 0) {
+    if (lane == 0) {
+      s->off[0] = 0;
+      s->off[1] = rows;
+      s->pre[0] = 0;
+      s->pre[1] = (rows + tile_rows - 1) / tile_rows;
+    }
+    return;
+  }
+  int run = 0;
+  bool bad = false;
+  for (int base = 0; base < groups; base += 32) {
+    const int e = base + lane;
+    int lo = 0, hi = 0;
+    if (e < groups) {
+      lo = offsets[e];
+      hi = offsets[e + 1];
+    }
+    bad |= lo < 0 || hi < lo || hi > rows;
+    int t = bad ? 0 : (hi - lo + tile_rows - 1) / tile_rows;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, t, d);
+      if (lane >= d) t += o;
+    }
+    if (e < groups) {
+      s->off[e] = lo;
+      s->pre[e + 1] = run + t;
+      if (e == groups - 1) s->off[groups] = hi;
+    }
+    run += __shfl_sync(0xffffffffu, t, 31);
+  }
+  if (lane == 0) s->pre[0] = 0;
+  if (__any_sync(0xffffffffu, bad)) {
+    __syncwarp();
+    for (int e = lane; e <= groups; e += 32) s->pre[e] = 0;
+    if (lane == 0 && dev_status) atomicCAS(dev_status, 0, kDevBadIndex);
+  }
+}
+
+// One tile: row tile `mt` of group e (rows row0 .. row0 + rows - 1 of the
+// matrix, scale block `block`), column tile nt.  `tile` only grows between
+// calls of one walker, so the group pointer moves forward.
+struct MxTile {
+  int e, mt, nt, row0, rows;
+};
+SVDQ_DEV MxTile mx_decode_tile(const MxSched* s, int tile, int tiles_n, int tile_rows, int& e) {
+  while (tile >= s->pre[e + 1] * tiles_n) ++e;
+  const int first = s->pre[e];
+  const int local = tile - first * tiles_n, mts = s->pre[e + 1] - first;
+  MxTile t;
+  t.e = e;
+  t.nt = local / mts;
+  t.mt = local - t.nt * mts;
+  t.row0 = s->off[e] + t.mt * tile_rows;
+  t.rows = min(s->off[e + 1] - t.row0, tile_rows);
+  return t;
+}
+
+// ------------------------------------------------------------------ products
+// Instruction descriptor of a block-scaled product of E2M1 operands with E8M0
+// scales; `step` (0 or 1) picks which two of the four scale bytes of a 32-bit
+// tensor-memory word this K = 64 step uses.
+SVDQ_DEV uint32_t mx_idesc(uint32_t m, uint32_t n, uint32_t step) {
+  return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24) | (step << 30) | (step << 5);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, E2M1 x E2M1, E8M0 scales per 32 (read from
+// tensor memory), fp32 accumulate.
+SVDQ_DEV void mma_mxfp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa_tmem,
+                        uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+SVDQ_DEV void mma_mxfp4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa_tmem,
+                             uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
+// Operand tiles: 128-byte rows in the 128-byte swizzle; scale tiles: rows of
+// 16 bytes, eight of them 128 bytes apart.
+SVDQ_DEV uint64_t mx_operand_desc(uint32_t saddr) { return smem_desc(saddr, 16, 1024, 2); }
+SVDQ_DEV uint64_t mx_scale_desc(uint32_t saddr) { return smem_desc(saddr, 0, 128, 0); }
+
+// ------------------------------------------------------------------ outputs
+SVDQ_DEV float mx_load16(const uint16_t* p, bool fp16) {
+  const uint16_t b = __ldg(p);
+  return fp16 ? __half2float(__ushort_as_half(b)) : __uint_as_float((uint32_t)b << 16);
+}
+// Two fp32 -> two 16-bit values (a in the low half), round to nearest even.
+SVDQ_DEV uint32_t mx_pack16(float a, float b, bool fp16) {
+  if (fp16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// g sigmoid(g) u.  The exponential and the quotient are the fast intrinsics
+// (relative error below 2^-20 for the |g| that leave sigmoid away from 0 and
+// 1): the value is rounded to 4 bits next.
+SVDQ_DEV float mx_swiglu(float g, float u) { return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u); }
+
+}  // namespace svdq

@@ -1,0 +1,527 @@
+// MXFP4 products with few rows per group: the weight as the M operand of the
+// tensor core, the rows (tokens) as its N operand.
+//
+//   D[n, m] = sum_b Xw[n, b] Xa[m, b] sum_{k in b} w[n, k] a[m, k]    (kind::mxf4)
+//   y[m, n] = round16(D[n, m] + bias[n])
+//   SwiGLU: two weights, gate and other: h = g sigmoid(g) u of their outputs,
+//   quantized to MXFP4 along n for the next product
+//
+// What bounds it: the weight bytes.  A group with m rows does m / 0.53
+// multiply-adds per weight byte, so below some 150 rows HBM is the limit and
+// the kernel is a weight stream: each CTA pulls 128 weight rows x 256 columns
+// (17 KB with their scales) per pipeline stage through TMA into a ring of
+// about 200 KB, which keeps ~30 MB in flight over the chip, and the rows ride
+// along as the narrow operand (N = 16 .. 128, as many as the tile has).
+// With the weight on the M side a tile of one row costs the tensor core
+// little more than its weight loads; with the rows on the M side (the pair
+// kernel) it would multiply 256 rows of padding.
+//
+// Schedule: tiles are (group, 128 weight rows, up to 128 rows); a persistent
+// CTA walks them, its producer running ahead into the next tile while the
+// epilogue drains the last (two accumulators in tensor memory).  With fewer
+// tiles than SMs and no groups to fill them, a cluster of 2, 4 or 8 CTAs
+// shares one tile's K range and adds its partial sums through distributed
+// shared memory, always in rank order.
+//
+// Roles (6 warps): 0-3 epilogue (tensor-memory lane quarter = warp), 4 TMA
+// producer, 5 MMA issuer.  Role loops run on whole warps and issue from one
+// elected lane.  Every mbarrier wait is bounded.
+#include "mxfp4.cuh"
+
+namespace svdq {
+namespace {
+
+constexpr int BW = 128;                 // weight rows per tile (MMA M)
+constexpr int BK_BYTES = 128;           // 256 elements of K per stage
+constexpr int EPI_WARPS = 4;
+constexpr int PRODUCER_WARP = 4, MMA_WARP = 5;
+constexpr int NUM_THREADS = 6 * 32;
+constexpr int W_BYTES = BW * BK_BYTES;  // 16 KB
+constexpr int SF_BYTES = 1024;          // 128 rows x 256 columns of scales
+constexpr int BOX_BYTES = kMxNarrowBox * BK_BYTES;
+constexpr int TMEM_COLS = 512;
+constexpr unsigned long long kDrainLimitNs = 2000000000ull;
+
+template <bool kGlu>
+struct Cfg {
+  static constexpr int kWeights = kGlu ? 2 : 1;                            // accumulators per tile
+  static constexpr int kRows = kGlu ? kMxNarrowRowsGlu : kMxNarrowRows;    // rows per tile (MMA N)
+  static constexpr int kStages = kGlu ? 5 : 6;
+  static constexpr int kActBytes = kRows * BK_BYTES;
+  static constexpr int kSfOff = kWeights * W_BYTES + kActBytes;            // SFW (per weight), then SFA
+  static constexpr int kStageBytes = kSfOff + (kWeights + 1) * SF_BYTES;
+  static constexpr int kAccCols = kWeights * kRows;                        // per accumulator buffer
+  static constexpr int kSfCols = 8 * kWeights + 8;
+  static constexpr int kTmemSf = 2 * kAccCols;
+  static constexpr int kStageOutBytes = kGlu ? 0 : 2 * 32 * BW * 2;        // two 32-row output staging buffers
+  static_assert(kStageBytes % 1024 == 0, "stages keep the 1024-byte alignment of SWIZZLE_128B");
+  static_assert(kTmemSf + kStages * kSfCols <= TMEM_COLS, "accumulators and scale buffers fit tensor memory");
+};
+
+struct Ctl {
+  uint64_t full[6];
+  uint64_t empty[6];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  MxSched sched;
+};
+
+template <bool kGlu>
+constexpr size_t smem_bytes() {
+  return 1024 + Cfg<kGlu>::kStages * Cfg<kGlu>::kStageBytes + Cfg<kGlu>::kStageOutBytes + sizeof(Ctl);
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "fits the shared memory of one CTA");
+static_assert(kMxNarrowRows * BW * 4 <= Cfg<false>::kStages * Cfg<false>::kStageBytes &&
+                  kMxNarrowRowsGlu * 2 * BW * 4 <= Cfg<true>::kStages * Cfg<true>::kStageBytes,
+              "partial sums reuse the ring");
+
+SVDQ_DEV float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <bool kGlu>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    mxfp4_gemm_narrow_kernel(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_w,
+                             const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfw,
+                             const MxGemmParams p) {
+  using C = Cfg<kGlu>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const out_base = smem + C::kStages * C::kStageBytes;
+  Ctl* const ctl = reinterpret_cast<Ctl*>(out_base + C::kStageOutBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&ctl->full[s]), 1);
+      mbar_init(smem_u32(&ctl->empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&ctl->acc_full[a]), 1);
+      mbar_init(smem_u32(&ctl->acc_empty[a]), EPI_WARPS);
+    }
+    mbar_init(smem_u32(&ctl->drain), 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == PRODUCER_WARP && lane == 0) {
+    prefetch_tmap(&tm_act);
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_sfa);
+    prefetch_tmap(&tm_sfw);
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(smem_u32(&ctl->tmem_base), TMEM_COLS);
+    tmem_relinquish();
+  }
+  // Offsets are an input like the weights: with weights_early both were
+  // complete before the preceding kernel began.
+  if (!p.weights_early) pdl_wait();
+  if (warp == 0) mx_build_sched(&ctl->sched, p.groups, p.offsets, p.rows, C::kRows, p.dev_status);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  pdl_launch_dependents();
+
+  const MxSched* const sched = &ctl->sched;
+  const int k_slices = (p.K + 255) / 256, k_chunks = (p.K + 127) / 128;
+  const int tiles_n = (p.N + BW - 1) / BW;
+  const int num_tiles = sched->pre[p.groups == 0 ? 1 : p.groups] * tiles_n;
+  const int splits = p.splits;
+  const uint32_t rank = splits > 1 ? cluster_ctarank() : 0;
+  // This CTA's part of K (whole K without splits) and its tiles.
+  const int kb_begin = (int)((long long)k_slices * (int)rank / splits);
+  const int kb_end = (int)((long long)k_slices * ((int)rank + 1) / splits);
+  const int t_first = (int)blockIdx.x / splits, t_step = (int)gridDim.x / splits;
+  const WaitCtx wctx{&ctl->abort_flag, p.dev_status, p.timeout_ns};
+
+  if (warp == PRODUCER_WARP) {
+    // -------------------------------------------------------------- producer
+    int stage = 0, e = 0;
+    uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+    bool ok = true, act_ready = !p.weights_early;
+    const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
+    auto issue_weight = [&](int st, const MxTile& t, int kb, int boxes) {
+      const uint32_t full = smem_u32(&ctl->full[st]);
+      const uint32_t base = smem_u32(smem + st * C::kStageBytes);
+      mbar_arrive_expect_tx(full, C::kWeights * (W_BYTES + SF_BYTES) + boxes * BOX_BYTES + SF_BYTES);
+#pragma unroll
+      for (int i = 0; i < C::kWeights; ++i) {
+        const int mat = t.e * C::kWeights + i;
+        tma_load_2d_hint(base + i * W_BYTES, &tm_w, kb * BK_BYTES, mat * p.N + t.nt * BW, full, pol_w);
+        tma_load_2d_hint(base + C::kSfOff + i * SF_BYTES, &tm_sfw, 0, ((mat * tiles_n + t.nt) * k_chunks + 2 * kb) * 2,
+                         full, pol_w);
+      }
+    };
+    auto issue_act = [&](int st, const MxTile& t, int kb, int boxes) {
+      const uint32_t full = smem_u32(&ctl->full[st]);
+      const uint32_t base = smem_u32(smem + st * C::kStageBytes);
+      for (int i = 0; i < boxes; ++i)
+        tma_load_2d_hint(base + C::kWeights * W_BYTES + i * BOX_BYTES, &tm_act, kb * BK_BYTES,
+                         t.row0 + i * kMxNarrowBox, full, pol_a);
+      const int block = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + t.mt * C::kRows / 128;
+      tma_load_2d_hint(base + C::kSfOff + C::kWeights * SF_BYTES, &tm_sfa, 0, (block * k_chunks + 2 * kb) * 2, full,
+                       pol_a);
+    };
+    for (int tile = t_first; tile < num_tiles && ok; tile += t_step) {
+      const MxTile t = mx_decode_tile(sched, tile, tiles_n, C::kRows, e);
+      const int boxes = (t.rows + kMxNarrowBox - 1) / kMxNarrowBox;
+      int kb = kb_begin;
+      if (!act_ready) {
+        // The first stages' weight side goes out while the kernel that makes
+        // the rows still runs; their row side follows once it is done.
+        const int n = min(kb_end - kb_begin, C::kStages);
+        if (elect_one())
+          for (int i = 0; i < n; ++i) issue_weight(i, t, kb_begin + i, boxes);
+        __syncwarp();
+        pdl_wait();
+        if (elect_one())
+          for (int i = 0; i < n; ++i) issue_act(i, t, kb_begin + i, boxes);
+        __syncwarp();
+        for (int i = 0; i < n; ++i) {
+          issued_mask |= 1u << stage;
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        kb += n;
+        act_ready = true;
+      }
+      for (; kb < kb_end; ++kb) {
+        if (!mbar_wait_warp(smem_u32(&ctl->empty[stage]), phase ^ 1, wctx, kDevTimeoutProducer)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          issue_weight(stage, t, kb, boxes);
+          issue_act(stage, t, kb, boxes);
+        }
+        __syncwarp();
+        issued_mask |= 1u << stage;
+        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!act_ready) pdl_wait();
+    // Never leave with copies in flight into shared memory.
+    volatile int never = 0;
+    const WaitCtx drain_ctx{&never, p.dev_status, kDrainLimitNs};
+    for (int s = 0; s < C::kStages; ++s)
+      if (issued_mask & (1u << s))
+        mbar_wait(smem_u32(&ctl->full[s]), (issued_phase >> s) & 1, drain_ctx, kDevTimeoutDrain);
+  } else if (warp == MMA_WARP) {
+    // -------------------------------------------------------------- MMA issuer
+    int stage = 0, e = 0, seq = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = t_first; tile < num_tiles && ok; tile += t_step, ++seq) {
+      const MxTile t = mx_decode_tile(sched, tile, tiles_n, C::kRows, e);
+      const int a = seq & 1;
+      if (!mbar_wait_warp(smem_u32(&ctl->acc_empty[a]), ((seq >> 1) & 1) ^ 1, wctx, kDevTimeoutMma)) break;
+      tc_fence_after();
+      const uint32_t n = (uint32_t)((t.rows + 15) & ~15);
+      const uint32_t idesc0 = mx_idesc(BW, n, 0), idesc1 = mx_idesc(BW, n, 1);
+      // The tile's rows within their 128-row scale block: 32 rows a column.
+      const uint32_t sfa_off = (uint32_t)((t.mt * C::kRows % 128) / 32);
+      for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if (!mbar_wait_warp(smem_u32(&ctl->full[stage]), phase, wctx, kDevTimeoutMma)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t base = smem_u32(smem + stage * C::kStageBytes);
+          const uint32_t sb = base + C::kWeights * W_BYTES;
+          const uint32_t sf = tmem + C::kTmemSf + stage * C::kSfCols;
+          // 64-column steps of this slice, and the 128-column scale tiles they read.
+          const int steps = min(4, (p.K - kb * 256 + 63) / 64);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (2 * j < steps) {
+#pragma unroll
+              for (int i = 0; i < C::kWeights; ++i)
+                tmem_cp_32x128_warpx4(sf + 8 * i + 4 * j, mx_scale_desc(base + C::kSfOff + i * SF_BYTES + 512 * j));
+              tmem_cp_32x128_warpx4(sf + 8 * C::kWeights + 4 * j,
+                                    mx_scale_desc(base + C::kSfOff + C::kWeights * SF_BYTES + 512 * j));
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if (s < steps) {
+#pragma unroll
+              for (int i = 0; i < C::kWeights; ++i)
+                mma_mxfp4(tmem + a * C::kAccCols + i * C::kRows, mx_operand_desc(base + i * W_BYTES + 32 * s),
+                          mx_operand_desc(sb + 32 * s), s & 1 ? idesc1 : idesc0, sf + 8 * i + 4 * (s >> 1),
+                          sf + 8 * C::kWeights + 4 * (s >> 1) + sfa_off, kb > kb_begin || s > 0 ? 1u : 0u);
+            }
+          }
+          tc_commit(smem_u32(&ctl->empty[stage]));
+        }
+        __syncwarp();
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) tc_commit(smem_u32(&ctl->acc_full[a]));
+      __syncwarp();
+    }
+    // Wait for every MMA before tensor memory is freed.
+    if (elect_one()) tc_commit(smem_u32(&ctl->drain));
+    __syncwarp();
+    volatile int never = 0;
+    const WaitCtx drain_ctx{&never, p.dev_status, kDrainLimitNs};
+    mbar_wait(smem_u32(&ctl->drain), 0, drain_ctx, kDevTimeoutDrain);
+  } else {
+    // -------------------------------------------------------------- epilogue
+    // Thread = weight row (output column); a tensor-memory column = a row of y.
+    const int q = warp;
+    const bool fp16 = p.fp16 != 0;
+    int e = 0, seq = 0, out_seq = 0;
+    for (int tile = t_first; tile < num_tiles; tile += t_step, ++seq) {
+      const MxTile t = mx_decode_tile(sched, tile, tiles_n, C::kRows, e);
+      const int a = seq & 1;
+      const int n0 = t.nt * BW, n = n0 + 32 * q + lane;
+      float b0 = 0.f, b1 = 0.f;
+      if (p.bias != nullptr && n < p.N && splits == 1) {
+        b0 = mx_load16(p.bias + (size_t)t.e * C::kWeights * p.N + n, fp16);
+        if constexpr (kGlu) b1 = mx_load16(p.bias + ((size_t)t.e * 2 + 1) * p.N + n, fp16);
+      }
+      const bool got = mbar_wait(smem_u32(&ctl->acc_full[a]), (seq >> 1) & 1, wctx, kDevTimeoutEpilogue);
+      if (named_bar_any(2, EPI_WARPS * 32, !got)) break;   // decided by all four warps
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * C::kAccCols);
+      const int chunks = (t.rows + 31) / 32;
+      for (int c = 0; c < chunks; ++c) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(acc + 32 * c, r);
+        if constexpr (kGlu) {
+          uint32_t r2[32];
+          tmem_ld_32x32b_x32(acc + C::kRows + 32 * c, r2);
+          tmem_ld_wait(r);
+          reg_fence(r2);
+          if (c == chunks - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->acc_empty[a]));
+          }
+          if (splits > 1) {
+            // Partial sums, [row][gate 128 | other 128] fp32 in the drained ring.
+            float* part = reinterpret_cast<float*>(smem) + 32 * c * 2 * BW + 32 * q + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              part[j * 2 * BW] = __uint_as_float(r[j]);
+              part[j * 2 * BW + BW] = __uint_as_float(r2[j]);
+            }
+            continue;
+          }
+          // 32 lanes = one block of 32 hidden columns (N % 32 == 0: a warp
+          // lies inside N or is padding of the last scale tile).
+          const bool in_n = n0 + 32 * q < p.N;
+          const int local = t.mt * C::kRows + 32 * c;   // row within the group
+          const int nblk = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + local / 128;
+          uint8_t* const sc = p.h_scales + mx_tile_offset(nblk, tiles_n, t.nt) + (local % 128) / 32 * 4 + q;
+          uint8_t* const codes = p.h_codes + (size_t)(t.row0 + 32 * c) * (p.N / 2) + (n0 + 32 * q) / 2;
+#pragma unroll
+          for (int j8 = 0; j8 < 32; j8 += 8) {
+            if (32 * c + j8 >= t.rows) break;
+            uint32_t word = 0, byte = 0;   // lane l: codes (its quarter) and scale of row j8 + l % 8
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float h = mx_swiglu(__fadd_rn(__uint_as_float(r[j8 + j]), b0),
+                                        __fadd_rn(__uint_as_float(r2[j8 + j]), b1));
+              const uint32_t t_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu);
+              const uint32_t sb = mx_scale_byte(t_bits);
+              const float v = __fmul_rn(h, mx_inv_scale(sb));
+              uint32_t code;
+              asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n\t"
+                  "mov.b32 %0, {x, x, x, x};\n\t}"
+                  : "=r"(code)
+                  : "f"(v), "f"(0.0f));
+              code = sb == 255u ? 0u : (code & 15u) << (4 * (lane & 7));
+              code |= __shfl_xor_sync(0xffffffffu, code, 1);
+              code |= __shfl_xor_sync(0xffffffffu, code, 2);
+              code |= __shfl_xor_sync(0xffffffffu, code, 4);
+              if ((lane & 7) == j) {
+                word = code;
+                byte = sb;
+              }
+            }
+            const int j = j8 + (lane & 7);
+            if (32 * c + j < t.rows) {
+              if (in_n) *reinterpret_cast<uint32_t*>(codes + (size_t)j * (p.N / 2) + 4 * (lane >> 3)) = word;
+              if (lane < 8) sc[j * 16] = in_n ? (uint8_t)byte : (uint8_t)0;
+            }
+          }
+        } else {
+          tmem_ld_wait(r);
+          if (c == chunks - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->acc_empty[a]));
+          }
+          if (splits > 1) {
+            // Partial sums, [row][128 weight rows] fp32 in the drained ring.
+            float* part = reinterpret_cast<float*>(smem) + 32 * c * BW + 32 * q + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) part[j * BW] = __uint_as_float(r[j]);
+            continue;
+          }
+          uint8_t* const buf = out_base + (out_seq & 1) * (32 * BW * 2);
+          ++out_seq;
+          uint16_t* const col = reinterpret_cast<uint16_t*>(buf) + 32 * q + lane;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const uint32_t w = mx_pack16(__fadd_rn(__uint_as_float(r[j]), b0),
+                                         __fadd_rn(__uint_as_float(r[j + 1]), b0), fp16);
+            col[j * BW] = (uint16_t)w;
+            col[(j + 1) * BW] = (uint16_t)(w >> 16);
+          }
+          // Two buffers: a thread rewrites one only after the barrier of the
+          // other, which every thread reaches after its reads of the first.
+          named_bar_sync(3, EPI_WARPS * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int v = threadIdx.x + 128 * i, j = v >> 4, x = v & 15;
+            if (32 * c + j < t.rows && n0 + 8 * x < p.N)
+              *reinterpret_cast<uint4*>(p.y + (size_t)(t.row0 + 32 * c + j) * p.ldy + n0 + 8 * x) =
+                  *reinterpret_cast<const uint4*>(buf + j * (BW * 2) + x * 16);
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  if (splits > 1) {
+    // Every CTA of the cluster has its partial sums in place (a cluster has
+    // one tile, or none); row j is added up by one warp of rank j mod splits,
+    // four columns a lane.
+    cluster_sync();
+    if (t_first < num_tiles) {
+      int e = 0;
+      const MxTile t = mx_decode_tile(sched, t_first, tiles_n, C::kRows, e);
+      const bool fp16 = p.fp16 != 0;
+      const int n = t.nt * BW + 4 * lane;
+      const bool in_n = n < p.N;          // N is a multiple of 8 (SwiGLU: 32)
+      float bias[C::kWeights][4];
+#pragma unroll
+      for (int w = 0; w < C::kWeights; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          bias[w][i] = p.bias != nullptr && in_n
+                           ? mx_load16(p.bias + ((size_t)t.e * C::kWeights + w) * p.N + n + i, fp16)
+                           : 0.f;
+      for (int j = (int)rank + splits * warp; j < t.rows; j += splits * (NUM_THREADS / 32)) {
+        float v[C::kWeights][4];
+#pragma unroll
+        for (int w = 0; w < C::kWeights; ++w) {
+          const uint32_t local = smem_u32(smem) + (uint32_t)((j * C::kWeights + w) * BW + 4 * lane) * 4;
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int r = 0; r < splits; ++r) {
+            const float4 o = ld_cluster_f4(mapa_shared(local, (uint32_t)r));
+            s = make_float4(__fadd_rn(s.x, o.x), __fadd_rn(s.y, o.y), __fadd_rn(s.z, o.z), __fadd_rn(s.w, o.w));
+          }
+          v[w][0] = __fadd_rn(s.x, bias[w][0]);
+          v[w][1] = __fadd_rn(s.y, bias[w][1]);
+          v[w][2] = __fadd_rn(s.z, bias[w][2]);
+          v[w][3] = __fadd_rn(s.w, bias[w][3]);
+        }
+        if constexpr (kGlu) {
+          // Eight lanes hold one block of 32 hidden columns.
+          uint32_t top = 0;
+          float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[i] = mx_swiglu(v[0][i], v[1][i]);
+            top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+          }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          const uint32_t sb = mx_scale_byte(top);
+          const float inv = mx_inv_scale(sb);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = __fmul_rn(h[i], inv);
+          const uint32_t code = sb == 255u ? 0u : mx_e2m1x8(h);
+          const int local = t.mt * C::kRows + j;   // row within the group
+          const int block = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + local / 128;
+          if (in_n)
+            *reinterpret_cast<uint16_t*>(p.h_codes + (size_t)(t.row0 + j) * (p.N / 2) + n / 2) = (uint16_t)code;
+          if ((lane & 7) == 0)
+            p.h_scales[mx_tile_offset(block, tiles_n, t.nt) + (local & 31) * 16 + (local % 128) / 32 * 4 +
+                       (lane >> 3)] = in_n ? (uint8_t)sb : (uint8_t)0;
+        } else if (in_n) {
+          *reinterpret_cast<uint2*>(p.y + (size_t)(t.row0 + j) * p.ldy + n) =
+              make_uint2(mx_pack16(v[0][0], v[0][1], fp16), mx_pack16(v[0][2], v[0][3], fp16));
+        }
+      }
+    }
+    cluster_sync();   // no CTA leaves while its partial sums are being read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+template <bool kGlu>
+cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, int num_sms, cudaStream_t stream, bool pdl) {
+  using C = Cfg<kGlu>;
+  auto kernel = mxfp4_gemm_narrow_kernel<kGlu>;
+  constexpr int smem = (int)smem_bytes<kGlu>();
+  if (cudaError_t e = mx_allow_smem<mxfp4_gemm_narrow_kernel<kGlu>>(smem)) return e;
+  // As many tiles as the rows can make: every group's last tile may be short.
+  const long long groups = p.groups == 0 ? 1 : p.groups;
+  const long long by_rows = (long long)(p.rows + C::kRows - 1) / C::kRows;
+  const long long m_tiles = p.groups == 0 ? by_rows : std::min<long long>(p.rows, p.rows / C::kRows + groups);
+  const long long tiles = m_tiles * ((p.N + BW - 1) / BW);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.splits > 1 ? tiles * p.splits : std::min<long long>(tiles, num_sms)));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (p.splits > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)p.splits;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kernel, t.act, t.w, t.sfa, t.sfw, p);
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_gemm_narrow(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, int num_sms,
+                                     cudaStream_t stream, bool pdl) {
+  return swiglu ? launch_impl<true>(p, t, num_sms, stream, pdl) : launch_impl<false>(p, t, num_sms, stream, pdl);
+}
+
+}  // namespace svdq

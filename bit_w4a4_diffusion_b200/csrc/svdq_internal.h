@@ -2,6 +2,8 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 namespace svdq {
@@ -24,6 +26,7 @@ enum DeviceStatus : int {
   kDevTimeoutMma = 2,
   kDevTimeoutEpilogue = 3,
   kDevTimeoutDrain = 4,
+  kDevBadIndex = 5,       // MXFP4 row groups: an offset or a row index out of range
 };
 
 // INT4 rows -> exact fp16 operands for the fp16 tensor pipe (dequant_int4.cu):
@@ -239,6 +242,108 @@ struct AwqParams {
 };
 
 cudaError_t launch_awq(const AwqParams& p, int num_sms, cudaStream_t stream, bool pdl);
+
+// ------------------------------------------------------------------ MXFP4
+constexpr int kMxMaxGroups = 512;
+
+// Elements of x, y, bias and dequantized values (mxfp4_dtype).
+enum MxDtype : int { kMxBf16 = 0, kMxFp16 = 1, kMxFp32 = 2 };
+
+struct MxQuantParams {
+  int rows, K, dtype;
+  const void* x;          // [x_rows, K], rows ldx elements apart
+  long long ldx;
+  const int* row_index;   // [rows] into x, or null: row i is row i
+  int x_rows;
+  int groups;             // 0: one group of all rows
+  const int* offsets;     // [groups + 1]
+  uint8_t* codes;         // [rows, K/2]
+  uint8_t* scales;        // tiled E8M0
+  int* dev_status;
+};
+cudaError_t launch_mxfp4_quantize(const MxQuantParams& p, cudaStream_t stream, bool pdl);
+
+struct MxDequantParams {
+  int rows, K, dtype;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int groups;
+  const int* offsets;
+  void* out;              // [rows, K], rows ldo elements apart
+  long long ldo;
+  int* dev_status;
+};
+cudaError_t launch_mxfp4_dequantize(const MxDequantParams& p, cudaStream_t stream, bool pdl);
+
+// The products.  N: columns of y, or (SwiGLU) hidden columns I, the weight
+// then being two matrices [I, K] per group.
+struct MxGemmParams {
+  int rows, N, K;
+  int groups;             // 0: one group of all rows
+  const int* offsets;
+  const uint16_t* bias;   // 16-bit [groups or 1, N] ([.., 2, N] for SwiGLU) or null
+  int fp16;               // 16-bit type of bias and y
+  uint16_t* y;            // [rows, N], rows ldy elements apart (plain)
+  long long ldy;
+  uint8_t* h_codes;       // SwiGLU: [rows, N/2]
+  uint8_t* h_scales;      // SwiGLU: tiled, K = N
+  int weights_early;      // the weights and offsets were complete before the preceding kernel began
+  int splits;             // narrow kernel: CTAs (one cluster) that share a tile's K
+  int* dev_status;
+  unsigned long long timeout_ns;
+};
+// act / w: codes [rows, K/2] / [matrices * N, K/2]; sfa / sfw: scales as rows
+// of 256 bytes; y: 16-bit [rows, N] (pair kernel's plain epilogue only).
+struct MxGemmTmaps {
+  CUtensorMap act, w, sfa, sfw, y;
+};
+// 256 x 256 tiles on CTA pairs (SwiGLU: 256 rows x 128 hidden columns).
+cudaError_t launch_mxfp4_gemm_pair(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, cudaStream_t stream,
+                                   bool pdl);
+// 128 weight rows x up to 128 (SwiGLU: 64) rows per CTA, the weight as the
+// M operand; t.act's box is kMxNarrowBox rows.
+constexpr int kMxNarrowBox = 32;
+constexpr int kMxNarrowRows = 128, kMxNarrowRowsGlu = 64;
+cudaError_t launch_mxfp4_gemm_narrow(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, int num_sms,
+                                     cudaStream_t stream, bool pdl);
+
+// A value found once per device (0: not yet found; the finder gives > 0).
+constexpr int kMxMaxDevices = 64;
+template <class T>
+struct MxPerDevice {
+  std::atomic<T> v[kMxMaxDevices] = {};
+  template <class F>
+  cudaError_t get(T* out, F&& find) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= kMxMaxDevices) return cudaErrorInvalidDevice;
+    T got = v[dev].load(std::memory_order_acquire);
+    if (got == T{}) {
+      if (cudaError_t e = find(&got)) return e;
+      v[dev].store(got, std::memory_order_release);
+    }
+    *out = got;
+    return cudaSuccess;
+  }
+};
+// Opts a kernel into `bytes` of dynamic shared memory, once per device.
+template <auto kKernel>
+cudaError_t mx_allow_smem(int bytes) {
+  static MxPerDevice<int> done;
+  int got = 0;
+  return done.get(&got, [&](int* n) {
+    *n = bytes;
+    return cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+}
+
+// What the entry points of other files share with abi.cu: the device check
+// (SVDQ_OK and the SM count, or a status with its message), the caller's
+// status word or the library's, and whether SVDQ_PDL leaves dependent
+// launches on.
+int require_device(int* sms);
+int status_word(int** dev_status);
+bool pdl_enabled();
 
 // Records a message for svdq_last_error() and returns `status`.
 int record_error(int status, const char* fmt, ...);

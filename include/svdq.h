@@ -397,6 +397,120 @@ int awq_pack_weights(int N, int K, const uint16_t* W, uint8_t* qweight, uint16_t
 int awq_w4a16_linear(int M, int N, int K, const void* x, const void* qweight, const void* scales, const void* zeros,
                      const void* bias, void* y, void* stream);
 
+/* ------------------------------------------------------------------ MXFP4
+ * 4-bit microscaled floating point (OCP Microscaling Formats v1.0, MXFP4):
+ * E2M1 elements in blocks of 32 along K that share an E8M0 scale, one byte b
+ * standing for 2^(b - 127), 0xFF for NaN.  Unlike the layers above there is
+ * no smoothing, no low-rank branch and no tensor scale; weights are used as
+ * they are (pages: none of them has this format; it is what checkpoints of
+ * models with experts commonly hold).
+ *
+ *   Q(v), per block: t = max|v|, X = 2^max(floor(log2 t) - 2, -127),
+ *     byte = log2 X + 127, code = E2M1_rn_sat(v / X) (sign kept);
+ *     a block with a NaN or an infinity: byte 0xFF, codes 0 (every product
+ *     with it is NaN).
+ *   y[m] = round16( sum_b Xa Xw sum_{k in b} a w + bias ), summed in fp32.
+ *
+ * Layouts: codes [rows, K/2], two per byte, element 2j in the low nibble.
+ * Scales are tiled: 512-byte tiles of 128 rows x 4 blocks,
+ *     byte (row m, group g = k/32) at
+ *     ((m/128) * ceil(K/128) + g/4) * 512 + (m%32) * 16 + ((m%128)/32) * 4 + g%4,
+ * rows padded to 128, groups to a multiple of 4 (padding groups must be 0).
+ * Several matrices [N, K] one behind the other (weights of experts): codes
+ * [matrices * N, K/2], scales mxfp4_scale_bytes(N, K) bytes per matrix.
+ *
+ * Row groups ("grouped" calls): rows are sorted by group, group e owns rows
+ * [offsets[e], offsets[e+1]) and multiplies with weight e.  offsets is a
+ * device int32 [groups + 1], not decreasing, within [0, rows]; groups may be
+ * empty, and rows before offsets[0] or from offsets[groups] on belong to
+ * none: the outputs there are left as they were.  `rows` is the capacity the
+ * buffers have; nothing depends on the host knowing the offsets.  In a grouped
+ * scale buffer (mxfp4_grouped_scale_bytes) the rows of group e start at
+ * 128-row block offsets[e]/128 + e and are numbered from 0 there.
+ * Offsets that decrease or leave [0, rows], and row indices outside
+ * [0, x_rows), are reported as code 5 through dev_status / svdq_device_status;
+ * the products of such a call write nothing, a row with a bad index becomes
+ * NaN.
+ *
+ * All entry points: K % 32 == 0, N % 8 == 0, rows from 0 (nothing is done)
+ * to 2^30, groups 1 to 512.  dtype is the type of x, y and bias; the row
+ * strides ldx, ldy, ldo are in elements and multiples of 16 bytes.  Matrix
+ * and bias pointers are 16-byte, offsets and row_index 4-byte aligned.
+ * The conventions at the top of this file hold (streams, errors, dev_status,
+ * PDL). */
+typedef enum { MXFP4_BF16 = 0, MXFP4_FP16 = 1, MXFP4_FP32 = 2 } mxfp4_dtype;
+#define MXFP4_MAX_GROUPS 512
+#define SVDQ_DEV_BAD_INDEX 5 /* device status code: offsets or row_index out of range */
+
+/* Sizes in bytes, -1 for unsupported arguments.  groups == 0 in the
+ * workspace size: the dense layer. */
+long long mxfp4_scale_bytes(int rows, int K);
+long long mxfp4_grouped_scale_bytes(int groups, int rows, int K);
+long long mxfp4_workspace_bytes(int groups, int rows, int K);
+long long mxfp4_mlp_workspace_bytes(int groups, int rows, int K, int I);
+
+/* Host: weights bf16 [matrices, N, K] -> codes and tiled scales (bit for bit
+ * those of mxfp4_quantize), and scales between row-major
+ * [matrices, rows, K/32] and tiled. */
+int mxfp4_pack_weights(int matrices, int N, int K, const uint16_t* W, uint8_t* codes, uint8_t* scales);
+int mxfp4_scales_to_rowmajor(int matrices, int rows, int K, const uint8_t* tiled, uint8_t* rowmajor);
+int mxfp4_scales_from_rowmajor(int matrices, int rows, int K, const uint8_t* rowmajor, uint8_t* tiled);
+
+/* mxfp4_quantize: x (bf16, fp16 or fp32) -> codes [rows, K/2] and tiled
+ * scales.  With row_index (device int32 [rows]) row i is x[row_index[i]]: the
+ * gather of tokens to their experts.  With groups > 0 and offsets the scales
+ * are in the grouped layout (rows outside every group are skipped);
+ * groups == 0, offsets == NULL: one matrix.
+ * mxfp4_dequantize: the values (bf16 or fp32, both exact) of codes and
+ * scales. */
+int mxfp4_quantize(int dtype, int rows, int K, const void* x, long long ldx, const int* row_index, int x_rows,
+                   int groups, const int* offsets, void* codes, void* scales, int* dev_status, void* stream);
+int mxfp4_dequantize(int dtype, int rows, int K, const void* codes, const void* scales, int groups,
+                     const int* offsets, void* out, long long ldo, int* dev_status, void* stream);
+
+/* mxfp4_gemm: y [M, N] = A W^T + bias of quantized rows and weights; dtype
+ * bf16 or fp16, bias [N] or NULL.  mxfp4_grouped_gemm: the same per group,
+ * weights [groups, N, K], bias [groups, N] or NULL.
+ * mxfp4_linear, mxfp4_grouped_linear: mxfp4_quantize of x, then the product,
+ * on `stream`; workspace of mxfp4_workspace_bytes, which calls may share only
+ * if they do not overlap in time.
+ * The product runs on one of two kernels: 256 x 256 tiles on CTA pairs, or,
+ * with few rows per group, a weight stream with the rows as the narrow
+ * operand.  SVDQ_MXFP4_GEMM_KERNEL=pair or =narrow in the environment (read
+ * at every call) forces one; they differ in the order of fp32 sums. */
+int mxfp4_gemm(int dtype, int M, int N, int K, const void* act_codes, const void* act_scales, const void* w_codes,
+               const void* w_scales, const void* bias, void* y, long long ldy, int* dev_status, void* stream);
+int mxfp4_grouped_gemm(int dtype, int groups, int rows, int N, int K, const int* offsets, const void* act_codes,
+                       const void* act_scales, const void* w_codes, const void* w_scales, const void* bias, void* y,
+                       long long ldy, int* dev_status, void* stream);
+int mxfp4_linear(int dtype, int M, int N, int K, const void* x, long long ldx, const void* w_codes,
+                 const void* w_scales, const void* bias, void* y, long long ldy, void* workspace,
+                 long long workspace_bytes, int* dev_status, void* stream);
+int mxfp4_grouped_linear(int dtype, int groups, int rows, int N, int K, const void* x, long long ldx,
+                         const int* row_index, int x_rows, const int* offsets, const void* w_codes,
+                         const void* w_scales, const void* bias, void* y, long long ldy, void* workspace,
+                         long long workspace_bytes, int* dev_status, void* stream);
+
+/* mxfp4_grouped_gemm_swiglu_quant: an experts' up product whose output never
+ * leaves the chip.  Each group has two weights [I, K], the gate's and the
+ * other factor's (w_codes [groups, 2, I, K/2], scales per matrix, bias
+ * [groups, 2, I] or NULL, of type dtype):
+ *   g, u = the two products + bias (fp32);  h = g sigmoid(g) u;
+ *   h_codes [rows, I/2], h_scales (grouped layout, K = I) = Q(h).
+ * I % 32 == 0.
+ * mxfp4_grouped_mlp_swiglu: y = down(Q(h)), h from Q(x): mxfp4_quantize, the
+ * call above, mxfp4_grouped_gemm with down weights [groups, K, I], on
+ * `stream`; workspace of mxfp4_mlp_workspace_bytes. */
+int mxfp4_grouped_gemm_swiglu_quant(int dtype, int groups, int rows, int I, int K, const int* offsets,
+                                    const void* act_codes, const void* act_scales, const void* w_codes,
+                                    const void* w_scales, const void* bias, void* h_codes, void* h_scales,
+                                    int* dev_status, void* stream);
+int mxfp4_grouped_mlp_swiglu(int dtype, int groups, int rows, int K, int I, const void* x, long long ldx,
+                             const int* row_index, int x_rows, const int* offsets, const void* up_codes,
+                             const void* up_scales, const void* up_bias, const void* down_codes,
+                             const void* down_scales, const void* down_bias, void* y, long long ldy, void* workspace,
+                             long long workspace_bytes, int* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
