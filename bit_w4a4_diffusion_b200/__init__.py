@@ -444,20 +444,35 @@ def awq_w4a16_linear(x, w, bias=None, y=None, stream=None):
 
 MXFP4_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MXFP4_MAX_GROUPS = 512
+MXFP4_FUSED_ROWS = 16
+MXFP4_FUSED_GROUPED_ROWS = 64
 
 
 def mxfp4_scale_bytes(rows, K, groups=0):
     """Bytes of the tiled E8M0 scales of [rows, K]; with ``groups`` those of
-    the grouped layout."""
-    return int(lib.mxfp4_grouped_scale_bytes(groups, rows, K) if groups else lib.mxfp4_scale_bytes(rows, K))
+    the grouped layout.  -1 for unsupported arguments, as in the library
+    (computed here: every call needs it)."""
+    if rows < 0 or K <= 0 or K % 32 or not 0 <= groups <= MXFP4_MAX_GROUPS:
+        return -1
+    return (rows // 128 + groups if groups else (rows + 127) // 128) * ((K + 127) // 128) * 512
+
+
+def _mx_quantized_bytes(rows, K, groups):
+    """Codes and scales of [rows, K] in a workspace."""
+    scales = mxfp4_scale_bytes(rows, K, groups)
+    return -1 if scales < 0 else ((rows * (K // 2) + 255) & ~255) + ((scales + 255) & ~255)
 
 
 def mxfp4_workspace_bytes(rows, K, groups=0):
-    return int(lib.mxfp4_workspace_bytes(groups, rows, K))
+    """Workspace of mxfp4_linear or (``groups``) mxfp4_grouped_linear: 0 with
+    so few rows that the product quantizes x itself."""
+    need = _mx_quantized_bytes(rows, K, groups)
+    return min(need, 0) if rows <= (MXFP4_FUSED_GROUPED_ROWS if groups else MXFP4_FUSED_ROWS) else need
 
 
 def mxfp4_mlp_workspace_bytes(groups, rows, K, I):
-    return int(lib.mxfp4_mlp_workspace_bytes(groups, rows, K, I))
+    x, h = mxfp4_workspace_bytes(rows, K, groups), _mx_quantized_bytes(rows, I, groups)
+    return -1 if x < 0 or h < 0 or groups == 0 else x + h
 
 
 def mxfp4_pack_weights(W_bits):
@@ -502,10 +517,27 @@ def mxfp4_scales_from_rowmajor(rowmajor):
 def _mx_call(device, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current, on its current
     stream unless one is given."""
-    if device.index == torch.cuda.current_device():
-        return _check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)))
-    with torch.cuda.device(device):
-        return _check(fn(*args, torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)))
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+    if status != 0:
+        _check(status)
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The same handle without a Stream object (3 us of a call's 10), where this
+# torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _mx_empty(shape, dtype, device):
+    return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
 
 
 def _mx_rows(t, name, dtypes):
@@ -543,7 +575,7 @@ def _mx_groups(offsets, device):
 
 def _mx_out(y, rows, N, dtype, device):
     if y is None:
-        return torch.empty((rows, N), dtype=dtype, device=device), N
+        return _mx_empty((rows, N), dtype, device), N
     _, ldy = _mx_rows(y, "y", (dtype,))
     if y.shape != (rows, N) or y.device != device:
         raise ValueError(f"y must be [{rows}, {N}] on {device}")
@@ -551,13 +583,16 @@ def _mx_out(y, rows, N, dtype, device):
 
 
 def _mx_workspace(workspace, need, device):
+    """(tensor to keep until the launch, pointer, bytes)."""
     if need < 0:
         raise SvdqError(2, "unsupported shape")
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
         raise TypeError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def _mx_status(dev_status, device):
@@ -582,8 +617,7 @@ def mxfp4_quantize(x, offsets=None, row_index=None, out=None, dev_status=None, s
     if size < 0:
         raise SvdqError(2, f"unsupported shape rows={rows} K={K} groups={groups}")
     if out is None:
-        out = (torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
-               torch.empty(size, dtype=torch.uint8, device=dev))
+        out = (_mx_empty((rows, K // 2), torch.uint8, dev), torch.empty(size, dtype=torch.uint8, device=dev))
     codes, scales = out
     _mx_call(dev, stream, lib.mxfp4_quantize, dtype, rows, K, x.data_ptr(), ldx,
              _mx_like(row_index, "row_index", dev, torch.int32, rows), x_rows, groups, off,
@@ -602,8 +636,10 @@ def mxfp4_dequantize(codes, scales, offsets=None, dtype=torch.bfloat16, out=None
     rows, K = codes.shape[0], codes.shape[1] * 2
     groups, off = (0, None) if offsets is None else _mx_groups(offsets, dev)
     if out is None:
-        out = (torch.empty if offsets is None else torch.zeros)((rows, K), dtype=dtype, device=dev)
-    out, ldo = _mx_out(out, rows, K, dtype, dev)
+        out = _mx_empty((rows, K), dtype, dev) if offsets is None else torch.zeros((rows, K), dtype=dtype, device=dev)
+        ldo = K
+    else:
+        out, ldo = _mx_out(out, rows, K, dtype, dev)
     size = mxfp4_scale_bytes(rows, K, groups)
     if size < 0 or dtype not in (torch.bfloat16, torch.float32):
         raise SvdqError(2, f"unsupported shape or dtype: rows={rows} K={K} groups={groups} {dtype}")
@@ -655,9 +691,9 @@ def mxfp4_linear(x, w, bias=None, y=None, workspace=None, dev_status=None, strea
     N = w["N"]
     wc, ws = _mx_weight(w, "w", dev, N, K, 1)
     y, ldy = _mx_out(y, M, N, x.dtype, dev)
-    workspace = _mx_workspace(workspace, mxfp4_workspace_bytes(M, K), dev)
+    workspace, ws_ptr, ws_size = _mx_workspace(workspace, mxfp4_workspace_bytes(M, K), dev)
     _mx_call(dev, stream, lib.mxfp4_linear, dtype, M, N, K, x.data_ptr(), ldx, wc, ws,
-             _mx_like(bias, "bias", dev, x.dtype, N), y.data_ptr(), ldy, workspace.data_ptr(), workspace.numel(),
+             _mx_like(bias, "bias", dev, x.dtype, N), y.data_ptr(), ldy, ws_ptr, ws_size,
              _mx_status(dev_status, dev))
     return y
 
@@ -674,11 +710,10 @@ def mxfp4_grouped_linear(x, offsets, w, row_index=None, bias=None, y=None, works
     groups, off = _mx_groups(offsets, dev)
     wc, ws = _mx_weight(w, "w", dev, N, K, groups)
     y, ldy = _mx_out(y, rows, N, x.dtype, dev)
-    workspace = _mx_workspace(workspace, mxfp4_workspace_bytes(rows, K, groups), dev)
+    workspace, ws_ptr, ws_size = _mx_workspace(workspace, mxfp4_workspace_bytes(rows, K, groups), dev)
     _mx_call(dev, stream, lib.mxfp4_grouped_linear, dtype, groups, rows, N, K, x.data_ptr(), ldx,
              _mx_like(row_index, "row_index", dev, torch.int32, rows), x_rows, off, wc, ws,
-             _mx_like(bias, "bias", dev, x.dtype, groups * N), y.data_ptr(), ldy, workspace.data_ptr(),
-             workspace.numel(), _mx_status(dev_status, dev))
+             _mx_like(bias, "bias", dev, x.dtype, groups * N), y.data_ptr(), ldy, ws_ptr, ws_size, _mx_status(dev_status, dev))
     return y
 
 
@@ -701,8 +736,7 @@ def mxfp4_grouped_gemm_swiglu_quant(codes, scales, offsets, w, bias=None, dtype=
     if size < 0:
         raise SvdqError(2, f"unsupported shape rows={rows} I={width} groups={groups}")
     if out is None:
-        out = (torch.empty((rows, width // 2), dtype=torch.uint8, device=dev),
-               torch.empty(size, dtype=torch.uint8, device=dev))
+        out = (_mx_empty((rows, width // 2), torch.uint8, dev), torch.empty(size, dtype=torch.uint8, device=dev))
     h_codes, h_scales = out
     _mx_call(dev, stream, lib.mxfp4_grouped_gemm_swiglu_quant, MXFP4_DTYPES[dtype], groups, rows, width, K, off,
              _mx_like(codes, "codes", dev, torch.uint8, rows * (K // 2)),
@@ -727,10 +761,9 @@ def mxfp4_grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index=None, up_bias=N
     uc, us = _mx_weight(w_up, "w_up", dev, width, K, 2 * groups)
     dc, ds = _mx_weight(w_down, "w_down", dev, K, width, groups)
     y, ldy = _mx_out(y, rows, K, x.dtype, dev)
-    workspace = _mx_workspace(workspace, mxfp4_mlp_workspace_bytes(groups, rows, K, width), dev)
+    workspace, ws_ptr, ws_size = _mx_workspace(workspace, mxfp4_mlp_workspace_bytes(groups, rows, K, width), dev)
     _mx_call(dev, stream, lib.mxfp4_grouped_mlp_swiglu, dtype, groups, rows, K, width, x.data_ptr(), ldx,
              _mx_like(row_index, "row_index", dev, torch.int32, rows), x_rows, off, uc, us,
              _mx_like(up_bias, "up_bias", dev, x.dtype, 2 * groups * width), dc, ds,
-             _mx_like(down_bias, "down_bias", dev, x.dtype, groups * K), y.data_ptr(), ldy, workspace.data_ptr(),
-             workspace.numel(), _mx_status(dev_status, dev))
+             _mx_like(down_bias, "down_bias", dev, x.dtype, groups * K), y.data_ptr(), ldy, ws_ptr, ws_size, _mx_status(dev_status, dev))
     return y

@@ -31,7 +31,7 @@ SVDQ_DEV float mx_inv_scale(uint32_t byte) { return byte == 255u ? 0.f : __uint_
 
 // Eight fp32 -> four bytes of E2M1 codes, element 2i in bits 8i..8i+3 and
 // element 2i+1 in bits 8i+4..8i+7; RNE, satfinite.
-SVDQ_DEV uint32_t mx_e2m1x8(const float (&v)[8]) {
+SVDQ_DEV uint32_t mx_e2m1x8(const float2 (&v)[4]) {
   uint32_t out;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -40,9 +40,89 @@ SVDQ_DEV uint32_t mx_e2m1x8(const float (&v)[8]) {
       "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
       "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(out)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
   return out;
 }
+
+// ------------------------------------------------------------------ elements
+struct MxRaw16 {
+  uint4 w;
+};
+struct MxRaw32 {
+  uint4 a, b;
+};
+
+// Eight consecutive elements of a row: how they are loaded, their largest
+// magnitude in an order that integers keep (sign cleared; NaN and infinity on
+// top), and their fp32 values times a power of two.  16-bit magnitudes are
+// compared two at a time as 16-bit integers, which order like the values.
+SVDQ_DEV uint4 mx_load_vec(const void* p, bool reused) {
+  const uint4* q = static_cast<const uint4*>(p);
+  return reused ? __ldg(q) : __ldcs(q);
+}
+SVDQ_DEV uint32_t mx_top16x2(const uint4& w) {
+  const uint32_t m = 0x7FFF7FFFu;
+  return __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+}
+SVDQ_DEV uint32_t mx_halves_max(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+
+template <int kDtype>
+struct MxElems;
+template <>
+struct MxElems<kMxBf16> {
+  using Raw = MxRaw16;
+  static constexpr int kSize = 2;
+  static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0)}; }
+  static SVDQ_DEV Raw load(const uint8_t* x, bool reused) { return {mx_load_vec(x, reused)}; }
+  static SVDQ_DEV uint32_t top(const Raw& r) { return mx_top16x2(r.w); }
+  static SVDQ_DEV uint32_t top_max(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+  static SVDQ_DEV uint32_t top_bits(uint32_t m) { return mx_halves_max(m) << 16; }
+  static SVDQ_DEV void scaled(const Raw& r, float inv, float2 (&v)[4]) {
+    const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = __fmul2_rn(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)),
+                        make_float2(inv, inv));
+  }
+};
+template <>
+struct MxElems<kMxFp16> {
+  using Raw = MxRaw16;
+  static constexpr int kSize = 2;
+  static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0)}; }
+  static SVDQ_DEV Raw load(const uint8_t* x, bool reused) { return {mx_load_vec(x, reused)}; }
+  static SVDQ_DEV uint32_t top(const Raw& r) { return mx_top16x2(r.w); }
+  static SVDQ_DEV uint32_t top_max(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+  static SVDQ_DEV uint32_t top_bits(uint32_t m) {
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)mx_halves_max(m))));
+  }
+  static SVDQ_DEV void scaled(const Raw& r, float inv, float2 (&v)[4]) {
+    const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&w[i])), make_float2(inv, inv));
+  }
+};
+template <>
+struct MxElems<kMxFp32> {
+  using Raw = MxRaw32;
+  static constexpr int kSize = 4;
+  static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
+  static SVDQ_DEV Raw load(const uint8_t* x, bool reused) { return {mx_load_vec(x, reused), mx_load_vec(x + 16, reused)}; }
+  static SVDQ_DEV uint32_t top(const Raw& r) {
+    const uint32_t m = 0x7FFFFFFFu;
+    return max(max(max(r.a.x & m, r.a.y & m), max(r.a.z & m, r.a.w & m)),
+               max(max(r.b.x & m, r.b.y & m), max(r.b.z & m, r.b.w & m)));
+  }
+  static SVDQ_DEV uint32_t top_max(uint32_t a, uint32_t b) { return max(a, b); }
+  static SVDQ_DEV uint32_t top_bits(uint32_t m) { return m; }
+  static SVDQ_DEV void scaled(const Raw& r, float inv, float2 (&v)[4]) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = __fmul2_rn(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), make_float2(inv, inv));
+  }
+};
 
 // ------------------------------------------------------------------ layout
 // Scales: 512-byte tiles of 128 rows x 4 blocks (128 elements of K), the

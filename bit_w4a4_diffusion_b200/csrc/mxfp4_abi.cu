@@ -119,6 +119,10 @@ int quantize(const Device& d, int dtype, int rows, int K, const void* x, long lo
   return cuda_status(launch_mxfp4_quantize(p, stream, d.pdl), "mxfp4_quantize launch");
 }
 
+// Few enough rows that the narrow kernel quantizes x itself: one launch, no
+// workspace for x.
+bool fuses(int groups, int rows) { return rows <= (groups == 0 ? MXFP4_FUSED_ROWS : MXFP4_FUSED_GROUPED_ROWS); }
+
 // Which kernel a product takes; SVDQ_MXFP4_GEMM_KERNEL=pair or =narrow (read
 // at every call) forces one of them.
 bool use_pair(int groups, int rows, int N, int sms) {
@@ -147,29 +151,37 @@ struct Product {
   long long ldy;
   void *h_codes, *h_scales;   // SwiGLU
   bool swiglu, weights_early;
+  const void* x = nullptr;    // not null: the product quantizes x itself (act_* unused)
+  long long ldx = 0;
+  const int* row_index = nullptr;
+  int x_rows = 0;
 };
 
 int product(const Device& d, const Product& g, cudaStream_t stream) {
   const int k_chunks = (g.K + 127) / 128;
   const int groups = g.groups == 0 ? 1 : g.groups;
   const long long matrices = (long long)groups * (g.swiglu ? 2 : 1);
-  const bool pair = use_pair(g.groups, g.rows, g.N, d.sms);
+  const bool pair = g.x == nullptr && use_pair(g.groups, g.rows, g.N, d.sms);
   MxGemmTmaps t;
   const uint64_t sfa_rows = (uint64_t)scale_blocks(g.groups, g.rows) * k_chunks * 2;
   const uint64_t sfw_rows = (uint64_t)matrices * ((g.N + 127) / 128) * k_chunks * 2;
-  bool ok = encode_tmap_2d(&t.act, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.act_codes, g.K / 2, g.rows, g.K / 2, 128,
-                           pair ? 128 : kMxNarrowBox, CU_TENSOR_MAP_SWIZZLE_128B);
-  ok = ok && encode_tmap_2d(&t.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, g.K / 2, (uint64_t)matrices * g.N, g.K / 2,
-                            128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-  ok = ok && encode_tmap_2d(&t.sfa, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.act_scales, 256, sfa_rows, 256, 256, 4,
-                            CU_TENSOR_MAP_SWIZZLE_NONE);
+  bool ok = encode_tmap_2d(&t.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, g.K / 2, (uint64_t)matrices * g.N, g.K / 2,
+                           128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (g.x == nullptr) {
+    ok = ok && encode_tmap_2d(&t.act, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.act_codes, g.K / 2, g.rows, g.K / 2, 128,
+                              pair ? 128 : kMxNarrowBox, CU_TENSOR_MAP_SWIZZLE_128B);
+    ok = ok && encode_tmap_2d(&t.sfa, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.act_scales, 256, sfa_rows, 256, 256, 4,
+                              CU_TENSOR_MAP_SWIZZLE_NONE);
+  } else {
+    t.act = t.sfa = t.w;   // not read
+  }
   ok = ok && encode_tmap_2d(&t.sfw, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_scales, 256, sfw_rows, 256, 256, 4,
                             CU_TENSOR_MAP_SWIZZLE_NONE);
   if (pair && !g.swiglu)
     ok = ok && encode_tmap_2d(&t.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.y, g.N, g.rows, (uint64_t)g.ldy * 2, 32, 32,
                               CU_TENSOR_MAP_SWIZZLE_64B);
   else
-    t.y = t.act;   // not read
+    t.y = t.w;   // not read
   if (!ok) return record_error(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the MXFP4 product");
   MxGemmParams p{};
   p.rows = g.rows;
@@ -183,6 +195,10 @@ int product(const Device& d, const Product& g, cudaStream_t stream) {
   p.ldy = g.ldy;
   p.h_codes = static_cast<uint8_t*>(g.h_codes);
   p.h_scales = static_cast<uint8_t*>(g.h_scales);
+  p.x = g.x;
+  p.ldx = g.ldx;
+  p.row_index = g.row_index;
+  p.x_rows = g.x_rows;
   p.weights_early = g.weights_early && d.pdl;
   p.splits = 1;
   p.dev_status = d.status;
@@ -195,7 +211,7 @@ int product(const Device& d, const Product& g, cudaStream_t stream) {
   return cuda_status(launch_mxfp4_gemm_narrow(p, t, g.swiglu, d.sms, stream, d.pdl), "mxfp4_gemm_narrow launch");
 }
 
-// Workspace of a layer: codes, then scales.
+// Workspace of quantized rows: codes, then scales.
 long long ws_scales_offset(int rows, int K) { return round_up((long long)rows * (K / 2), 256); }
 long long ws_bytes(int groups, int rows, int K) {
   return ws_scales_offset(rows, K) + round_up(scale_bytes(scale_blocks(groups, rows), K), 256);
@@ -230,10 +246,17 @@ int linear(int dtype, int groups, int rows, int N, int K, const void* x, long lo
   if (int s = check_buffer(w_scales, "w_scales")) return s;
   if (!aligned(bias, 16)) return record_error(SVDQ_ERR_INVALID_ARG, "bias must be 16-byte aligned");
   if (int s = check_matrix(y, ldy, N, 2, "y")) return s;
-  if (int s = check_workspace(workspace, workspace_bytes, ws_bytes(groups, rows, K))) return s;
+  const bool fused = fuses(groups, rows);
+  if (!fused)
+    if (int s = check_workspace(workspace, workspace_bytes, ws_bytes(groups, rows, K))) return s;
   Device d;
   if (int s = device(dev_status, &d)) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (fused) {
+    Product g{dtype, rows, N, K, groups, offsets, nullptr, nullptr, w_codes, w_scales, bias, y, ldy, nullptr, nullptr,
+              false, false, x, ldx, row_index, x_rows};
+    return product(d, g, st);
+  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   void* scales = ws + ws_scales_offset(rows, K);
   if (int s = quantize(d, dtype, rows, K, x, ldx, row_index, x_rows, groups, offsets, ws, scales, st)) return s;
@@ -258,12 +281,13 @@ long long mxfp4_grouped_scale_bytes(int groups, int rows, int K) {
 
 long long mxfp4_workspace_bytes(int groups, int rows, int K) {
   if (groups < 0 || groups > kMxMaxGroups || rows < 0 || K <= 0 || K % 32 != 0) return -1;
-  return ws_bytes(groups, rows, K);
+  return fuses(groups, rows) ? 0 : ws_bytes(groups, rows, K);
 }
 
 long long mxfp4_mlp_workspace_bytes(int groups, int rows, int K, int I) {
-  const long long a = mxfp4_workspace_bytes(groups, rows, K), b = mxfp4_workspace_bytes(groups, rows, I);
-  return a < 0 || b < 0 || groups == 0 ? -1 : a + b;
+  const long long x = mxfp4_workspace_bytes(groups, rows, K);
+  if (x < 0 || groups == 0 || I <= 0 || I % 32 != 0) return -1;
+  return x + ws_bytes(groups, rows, I);
 }
 
 int mxfp4_quantize(int dtype, int rows, int K, const void* x, long long ldx, const int* row_index, int x_rows,
@@ -386,10 +410,19 @@ int mxfp4_grouped_mlp_swiglu(int dtype, int groups, int rows, int K, int I, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint8_t* xs = ws + ws_scales_offset(rows, K);
-  uint8_t* h = ws + ws_bytes(groups, rows, K);
+  const bool fused = fuses(groups, rows);
+  uint8_t* h = ws + (fused ? 0 : ws_bytes(groups, rows, K));
   uint8_t* hs = h + ws_scales_offset(rows, I);
-  if (int s = quantize(d, dtype, rows, K, x, ldx, row_index, x_rows, groups, offsets, ws, xs, st)) return s;
   Product up{dtype, rows, I, K, groups, offsets, ws, xs, up_codes, up_scales, up_bias, nullptr, 0, h, hs, true, true};
+  if (fused) {
+    up.x = x;
+    up.ldx = ldx;
+    up.row_index = row_index;
+    up.x_rows = x_rows;
+    up.weights_early = false;
+  } else if (int s = quantize(d, dtype, rows, K, x, ldx, row_index, x_rows, groups, offsets, ws, xs, st)) {
+    return s;
+  }
   if (int s = product(d, up, st)) return s;
   Product down{dtype, rows, K, I, groups, offsets, h, hs, down_codes, down_scales, down_bias, y, ldy, nullptr,
                nullptr, false, true};

@@ -23,9 +23,15 @@
 // shares one tile's K range and adds its partial sums through distributed
 // shared memory, always in rank order.
 //
+// With a handful of rows the quantizer runs inside (kX): four more warps read
+// x, a K slice each in turn, and write the codes and scale bytes of the row
+// operand straight into the stage, in the layout TMA would have left.  Every
+// tile repeats that work, which is little for few rows, and the layer is one
+// launch instead of two.
+//
 // Roles (6 warps): 0-3 epilogue (tensor-memory lane quarter = warp), 4 TMA
-// producer, 5 MMA issuer.  Role loops run on whole warps and issue from one
-// elected lane.  Every mbarrier wait is bounded.
+// producer, 5 MMA issuer; kX: 6-9 quantizer.  Role loops run on whole warps
+// and issue from one elected lane.  Every mbarrier wait is bounded.
 #include "mxfp4.cuh"
 
 namespace svdq {
@@ -35,7 +41,11 @@ constexpr int BW = 128;                 // weight rows per tile (MMA M)
 constexpr int BK_BYTES = 128;           // 256 elements of K per stage
 constexpr int EPI_WARPS = 4;
 constexpr int PRODUCER_WARP = 4, MMA_WARP = 5;
-constexpr int NUM_THREADS = 6 * 32;
+constexpr int QUANT_WARP = 6, QUANT_WARPS = 4;
+constexpr int kNoX = -1;                // kX: x quantized beforehand, or x's dtype
+template <int kX>
+constexpr int num_threads() { return (QUANT_WARP + (kX == kNoX ? 0 : QUANT_WARPS)) * 32; }
+constexpr int MAX_SPLITS = 8;
 constexpr int W_BYTES = BW * BK_BYTES;  // 16 KB
 constexpr int SF_BYTES = 1024;          // 128 rows x 256 columns of scales
 constexpr int BOX_BYTES = kMxNarrowBox * BK_BYTES;
@@ -87,12 +97,13 @@ SVDQ_DEV float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-template <bool kGlu>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+template <bool kGlu, int kX>
+__global__ void __launch_bounds__(num_threads<kX>(), 1)
     mxfp4_gemm_narrow_kernel(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_w,
                              const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfw,
                              const MxGemmParams p) {
   using C = Cfg<kGlu>;
+  constexpr bool kFused = kX != kNoX;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const out_base = smem + C::kStages * C::kStageBytes;
@@ -101,7 +112,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(smem_u32(&ctl->full[s]), 1);
+      mbar_init(smem_u32(&ctl->full[s]), kFused ? 2 : 1);   // the producer, and a quantizer warp
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -113,9 +124,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     fence_mbar_init();
   }
   if (warp == PRODUCER_WARP && lane == 0) {
-    prefetch_tmap(&tm_act);
+    if (!kFused) {
+      prefetch_tmap(&tm_act);
+      prefetch_tmap(&tm_sfa);
+    }
     prefetch_tmap(&tm_w);
-    prefetch_tmap(&tm_sfa);
     prefetch_tmap(&tm_sfw);
   }
   if (warp == MMA_WARP) {
@@ -154,7 +167,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     auto issue_weight = [&](int st, const MxTile& t, int kb, int boxes) {
       const uint32_t full = smem_u32(&ctl->full[st]);
       const uint32_t base = smem_u32(smem + st * C::kStageBytes);
-      mbar_arrive_expect_tx(full, C::kWeights * (W_BYTES + SF_BYTES) + boxes * BOX_BYTES + SF_BYTES);
+      mbar_arrive_expect_tx(full,
+                            C::kWeights * (W_BYTES + SF_BYTES) + (kFused ? 0 : boxes * BOX_BYTES + SF_BYTES));
 #pragma unroll
       for (int i = 0; i < C::kWeights; ++i) {
         const int mat = t.e * C::kWeights + i;
@@ -164,6 +178,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     };
     auto issue_act = [&](int st, const MxTile& t, int kb, int boxes) {
+      if (kFused) return;
       const uint32_t full = smem_u32(&ctl->full[st]);
       const uint32_t base = smem_u32(smem + st * C::kStageBytes);
       for (int i = 0; i < boxes; ++i)
@@ -236,7 +251,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t n = (uint32_t)((t.rows + 15) & ~15);
       const uint32_t idesc0 = mx_idesc(BW, n, 0), idesc1 = mx_idesc(BW, n, 1);
       // The tile's rows within their 128-row scale block: 32 rows a column.
-      const uint32_t sfa_off = (uint32_t)((t.mt * C::kRows % 128) / 32);
+      const uint32_t sfa_off = kFused ? 0u : (uint32_t)((t.mt * C::kRows % 128) / 32);
       for (int kb = kb_begin; kb < kb_end; ++kb) {
         if (!mbar_wait_warp(smem_u32(&ctl->full[stage]), phase, wctx, kDevTimeoutMma)) {
           ok = false;
@@ -287,6 +302,75 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     volatile int never = 0;
     const WaitCtx drain_ctx{&never, p.dev_status, kDrainLimitNs};
     mbar_wait(smem_u32(&ctl->drain), 0, drain_ctx, kDevTimeoutDrain);
+  } else if (kFused && warp >= QUANT_WARP) {
+    // -------------------------------------------------------------- quantizer
+    // Warp w takes every fourth K slice: lane l the eight columns 8 l .. + 7
+    // of the slice, four lanes a block.  x is read while the stage is still
+    // in use; a slice's rows come eight at a time.
+    if constexpr (kFused) {
+      using E = MxElems<kX>;
+      const int l8 = 8 * lane;
+      int count = 0, e = 0;    // slices of all tiles so far
+      bool ok = true;
+      for (int tile = t_first; tile < num_tiles && ok; tile += t_step) {
+        const MxTile t = mx_decode_tile(sched, tile, tiles_n, C::kRows, e);
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++count) {
+          if ((count & (QUANT_WARPS - 1)) != warp - QUANT_WARP) continue;
+          const int stage = count % C::kStages;
+          const uint32_t phase = (uint32_t)(count / C::kStages) & 1;
+          const int k = kb * 256 + l8;
+          const bool k_ok = k < p.K;
+          uint8_t* const act = smem + stage * C::kStageBytes + C::kWeights * W_BYTES;
+          uint8_t* const sf = smem + stage * C::kStageBytes + C::kSfOff + C::kWeights * SF_BYTES +
+                              (lane >> 4) * 512 + ((lane >> 2) & 3);
+          bool waited = false;
+          for (int r0 = 0; r0 < t.rows; r0 += 8) {
+            typename E::Raw raw[8];
+            uint32_t lost = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              raw[i] = E::zero();
+              if (r0 + i < t.rows) {
+                int src = t.row0 + r0 + i;
+                if (p.row_index != nullptr) {
+                  src = __ldg(p.row_index + src);
+                  if (src < 0 || src >= p.x_rows) lost |= 1u << i;
+                }
+                if (k_ok && !((lost >> i) & 1u))
+                  raw[i] = E::load(static_cast<const uint8_t*>(p.x) + ((size_t)src * p.ldx + k) * E::kSize, true);
+              }
+            }
+            if (lost && p.dev_status) atomicCAS(p.dev_status, 0, kDevBadIndex);
+            if (!waited) {
+              if (!mbar_wait_warp(smem_u32(&ctl->empty[stage]), phase ^ 1, wctx, kDevTimeoutProducer)) {
+                ok = false;
+                break;
+              }
+              waited = true;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = r0 + i;
+              if (r >= t.rows) break;
+              uint32_t m = E::top(raw[i]);
+              m = E::top_max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+              m = E::top_max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+              const uint32_t b = (lost >> i) & 1u ? 255u : mx_scale_byte(E::top_bits(m));
+              float2 v[4];
+              E::scaled(raw[i], mx_inv_scale(b), v);
+              // 128-byte rows, 16-byte chunks XOR-ed by the row: SWIZZLE_128B.
+              *reinterpret_cast<uint32_t*>(act + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) =
+                  b == 255u ? 0u : mx_e2m1x8(v);
+              if ((lane & 3) == 0) sf[(r & 31) * 16 + (r >> 5) * 4] = k_ok ? (uint8_t)b : (uint8_t)0;
+            }
+          }
+          if (!ok) break;
+          fence_proxy_async_smem();   // the tensor core reads through the async proxy
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->full[stage]));
+        }
+      }
+    }
   } else {
     // -------------------------------------------------------------- epilogue
     // Thread = weight row (output column); a tensor-memory column = a row of y.
@@ -427,16 +511,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           bias[w][i] = p.bias != nullptr && in_n
                            ? mx_load16(p.bias + ((size_t)t.e * C::kWeights + w) * p.N + n + i, fp16)
                            : 0.f;
-      for (int j = (int)rank + splits * warp; j < t.rows; j += splits * (NUM_THREADS / 32)) {
+      for (int j = (int)rank + splits * warp; j < t.rows; j += splits * (num_threads<kX>() / 32)) {
         float v[C::kWeights][4];
 #pragma unroll
         for (int w = 0; w < C::kWeights; ++w) {
           const uint32_t local = smem_u32(smem) + (uint32_t)((j * C::kWeights + w) * BW + 4 * lane) * 4;
-          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int r = 0; r < splits; ++r) {
-            const float4 o = ld_cluster_f4(mapa_shared(local, (uint32_t)r));
-            s = make_float4(__fadd_rn(s.x, o.x), __fadd_rn(s.y, o.y), __fadd_rn(s.z, o.z), __fadd_rn(s.w, o.w));
-          }
+          float4 o[MAX_SPLITS];   // all on their way before the first is added
+#pragma unroll
+          for (int r = 0; r < MAX_SPLITS; ++r)
+            if (r < splits) o[r] = ld_cluster_f4(mapa_shared(local, (uint32_t)r));
+          float4 s = o[0];
+#pragma unroll
+          for (int r = 1; r < MAX_SPLITS; ++r)
+            if (r < splits)
+              s = make_float4(__fadd_rn(s.x, o[r].x), __fadd_rn(s.y, o[r].y), __fadd_rn(s.z, o[r].z),
+                              __fadd_rn(s.w, o[r].w));
           v[w][0] = __fadd_rn(s.x, bias[w][0]);
           v[w][1] = __fadd_rn(s.y, bias[w][1]);
           v[w][2] = __fadd_rn(s.z, bias[w][2]);
@@ -445,7 +534,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if constexpr (kGlu) {
           // Eight lanes hold one block of 32 hidden columns.
           uint32_t top = 0;
-          float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          float h[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             h[i] = mx_swiglu(v[0][i], v[1][i]);
@@ -456,9 +545,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
           const uint32_t sb = mx_scale_byte(top);
           const float inv = mx_inv_scale(sb);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = __fmul_rn(h[i], inv);
-          const uint32_t code = sb == 255u ? 0u : mx_e2m1x8(h);
+          const float2 v2[4] = {make_float2(__fmul_rn(h[0], inv), __fmul_rn(h[1], inv)),
+                                make_float2(__fmul_rn(h[2], inv), __fmul_rn(h[3], inv)), make_float2(0.f, 0.f),
+                                make_float2(0.f, 0.f)};
+          const uint32_t code = sb == 255u ? 0u : mx_e2m1x8(v2);
           const int local = t.mt * C::kRows + j;   // row within the group
           const int block = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + local / 128;
           if (in_n)
@@ -482,12 +572,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-template <bool kGlu>
+template <bool kGlu, int kX>
 cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, int num_sms, cudaStream_t stream, bool pdl) {
   using C = Cfg<kGlu>;
-  auto kernel = mxfp4_gemm_narrow_kernel<kGlu>;
+  auto kernel = mxfp4_gemm_narrow_kernel<kGlu, kX>;
   constexpr int smem = (int)smem_bytes<kGlu>();
-  if (cudaError_t e = mx_allow_smem<mxfp4_gemm_narrow_kernel<kGlu>>(smem)) return e;
+  if (cudaError_t e = mx_allow_smem<mxfp4_gemm_narrow_kernel<kGlu, kX>>(smem)) return e;
   // As many tiles as the rows can make: every group's last tile may be short.
   const long long groups = p.groups == 0 ? 1 : p.groups;
   const long long by_rows = (long long)(p.rows + C::kRows - 1) / C::kRows;
@@ -495,7 +585,7 @@ cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, int num_sms
   const long long tiles = m_tiles * ((p.N + BW - 1) / BW);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.splits > 1 ? tiles * p.splits : std::min<long long>(tiles, num_sms)));
-  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.blockDim = dim3(num_threads<kX>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -521,7 +611,14 @@ cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, int num_sms
 
 cudaError_t launch_mxfp4_gemm_narrow(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, int num_sms,
                                      cudaStream_t stream, bool pdl) {
-  return swiglu ? launch_impl<true>(p, t, num_sms, stream, pdl) : launch_impl<false>(p, t, num_sms, stream, pdl);
+  if (p.x == nullptr)
+    return swiglu ? launch_impl<true, kNoX>(p, t, num_sms, stream, pdl)
+                  : launch_impl<false, kNoX>(p, t, num_sms, stream, pdl);
+  if (p.fp16)
+    return swiglu ? launch_impl<true, kMxFp16>(p, t, num_sms, stream, pdl)
+                  : launch_impl<false, kMxFp16>(p, t, num_sms, stream, pdl);
+  return swiglu ? launch_impl<true, kMxBf16>(p, t, num_sms, stream, pdl)
+                : launch_impl<false, kMxBf16>(p, t, num_sms, stream, pdl);
 }
 
 }  // namespace svdq

@@ -324,9 +324,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float v[8];
+            float2 v[4];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = __fmul_rn(__uint_as_float(r[i][8 * j + x]), inv);
+            for (int x = 0; x < 4; ++x)
+              v[x] = __fmul2_rn(make_float2(__uint_as_float(r[i][8 * j + 2 * x]),
+                                            __uint_as_float(r[i][8 * j + 2 * x + 1])),
+                                make_float2(inv, inv));
             w[j] = sb == 255u ? 0u : mx_e2m1x8(v);
           }
           const bool in_n = nw + 32 * i < p.N;              // N % 32 == 0

@@ -23,6 +23,16 @@ constexpr int MQ_WARPS = 8;
 constexpr int MQ_THREADS = MQ_WARPS * 32;
 constexpr int MQ_COLS = 256;
 
+// A CTA's scale block and column slice; with parts = 4 it has one of the four
+// row quads of each warp instead of all four.
+struct Place {
+  int block, slice, part;
+};
+SVDQ_DEV Place place(int k_slices, int parts) {
+  const unsigned tile = blockIdx.x / (unsigned)parts, block = tile / (unsigned)k_slices;
+  return {(int)block, (int)(tile - block * k_slices), (int)(blockIdx.x - tile * parts)};
+}
+
 // The rows of scale block `block`: first row, how many (at most 128), and
 // whether the block belongs to a group with sound offsets.  Every lane of the
 // warp gets the same answer.
@@ -53,68 +63,14 @@ SVDQ_DEV bool find_block(int block, int rows, int groups, const int* offsets, in
   return true;
 }
 
-struct Raw16 {
-  uint4 w;
-};
-struct Raw32 {
-  uint4 a, b;
-};
-
 template <int kDtype>
-struct Elems;
-template <>
-struct Elems<kMxBf16> {
-  using Raw = Raw16;
-  static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0)}; }
-  static SVDQ_DEV Raw load(const void* x, size_t i) {
-    return {__ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i))};
-  }
-  static SVDQ_DEV void to_float(const Raw& r, float (&v)[8]) {
-    const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-};
-template <>
-struct Elems<kMxFp16> {
-  using Raw = Raw16;
-  static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0)}; }
-  static SVDQ_DEV Raw load(const void* x, size_t i) { return Elems<kMxBf16>::load(x, i); }
-  static SVDQ_DEV void to_float(const Raw& r, float (&v)[8]) {
-    const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-};
-template <>
-struct Elems<kMxFp32> {
-  using Raw = Raw32;
-  static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
-  static SVDQ_DEV Raw load(const void* x, size_t i) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + i);
-    return {__ldcs(p), __ldcs(p + 1)};
-  }
-  static SVDQ_DEV void to_float(const Raw& r, float (&v)[8]) {
-    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-  }
-};
-
-template <int kDtype>
-__global__ void __launch_bounds__(MQ_THREADS) mxfp4_quantize_kernel(const MxQuantParams p, int k_slices) {
-  using E = Elems<kDtype>;
+__global__ void __launch_bounds__(MQ_THREADS) mxfp4_quantize_kernel(const MxQuantParams p, int k_slices, int parts) {
+  using E = MxElems<kDtype>;
   pdl_wait();
   // Every CTA of this grid has begun by the time a dependent kernel starts.
   pdl_launch_dependents();
-  const int block = (int)(blockIdx.x / (unsigned)k_slices), slice = (int)(blockIdx.x - (unsigned)block * k_slices);
+  const Place at = place(k_slices, parts);
+  const int block = at.block, slice = at.slice;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int row0, count;
   if (!find_block(block, p.rows, p.groups, p.offsets, p.dev_status, row0, count)) return;
@@ -124,45 +80,50 @@ __global__ void __launch_bounds__(MQ_THREADS) mxfp4_quantize_kernel(const MxQuan
   const int k = slice * MQ_COLS + half * 128 + 8 * l;
   const bool k_ok = k < p.K;                            // uniform over a block's four lanes
   const int chunk = slice * 2 + half;
-  uint8_t* const sc = p.scales + mx_tile_offset(block, k_chunks, chunk);
+  uint8_t* const sc = p.scales + mx_tile_offset(block, k_chunks, chunk) + 4 * l;
+  const uint8_t* const x = static_cast<const uint8_t*>(p.x) + (size_t)k * E::kSize;
+  const size_t pitch = (size_t)p.ldx * E::kSize;
+  const bool gather = p.row_index != nullptr;
 
-  for (int r = warp; r < 32 && r < count; r += MQ_WARPS) {
-    typename E::Raw raw[4];
-    uint32_t lost = 0;                                  // rows whose index is out of range
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int rr = r + 32 * i;
-      raw[i] = E::zero();
-      if (rr < count) {
-        long long src = row0 + rr;
-        if (p.row_index != nullptr) {
-          src = __ldg(p.row_index + src);
-          if (src < 0 || src >= p.x_rows) {
-            lost |= 1u << i;
-            src = -1;
-          }
+  // The warp's rows are warp + 8 t + 32 i for t, i < 4; lane 4 t + i holds
+  // where row (t, i) comes from: -1 past the block's rows, -2 out of range.
+  int src = -1;
+  {
+    const int rr = warp + MQ_WARPS * (l >> 2) + 32 * (l & 3);
+    if (rr < count) {
+      src = row0 + rr;
+      if (gather) {
+        src = __ldg(p.row_index + src);
+        if (src < 0 || src >= p.x_rows) {
+          src = -2;
+          if (p.dev_status) atomicCAS(p.dev_status, 0, kDevBadIndex);
         }
-        if (k_ok && src >= 0) raw[i] = E::load(p.x, (size_t)src * p.ldx + k);
       }
     }
-    if (lost && p.dev_status) atomicCAS(p.dev_status, 0, kDevBadIndex);
+  }
+  auto load_quad = [&](int t, typename E::Raw (&raw)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = __shfl_sync(0xffffffffu, src, 4 * t + i);
+      raw[i] = s >= 0 && k_ok ? E::load(x + (size_t)s * pitch, gather) : E::zero();
+    }
+  };
+  auto finish_quad = [&](int t, const typename E::Raw (&raw)[4]) {
+    const int r = warp + MQ_WARPS * t;
     uint32_t mine = 0;                                  // byte i: the scale of row r + 32 i, this lane's block
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float v[8];
-      E::to_float(raw[i], v);
-      uint32_t t = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t = max(t, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-      t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
-      t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      const uint32_t b = (lost >> i) & 1u ? 255u : mx_scale_byte(t);
-      const float inv = mx_inv_scale(b);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
+      const int s = __shfl_sync(0xffffffffu, src, 4 * t + i);
+      if (s == -1) continue;                            // the same in every lane
+      uint32_t m = E::top(raw[i]);
+      m = E::top_max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = E::top_max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t b = s == -2 ? 255u : mx_scale_byte(E::top_bits(m));
+      float2 v[4];
+      E::scaled(raw[i], mx_inv_scale(b), v);
       const uint32_t w = b == 255u ? 0u : mx_e2m1x8(v);
       mine |= (k_ok ? b : 0u) << (8 * i);
-      if (k_ok && r + 32 * i < count)
+      if (k_ok)
         *reinterpret_cast<uint32_t*>(p.codes + (size_t)(row0 + r + 32 * i) * (p.K / 2) + k / 2) = w;
     }
     // Lanes 0..3 of the chunk collect one row's four group bytes each.
@@ -170,22 +131,40 @@ __global__ void __launch_bounds__(MQ_THREADS) mxfp4_quantize_kernel(const MxQuan
                    g2 = __shfl_sync(0xffffffffu, mine, half * 16 + 8),
                    g3 = __shfl_sync(0xffffffffu, mine, half * 16 + 12);
     if (l < 4 && chunk < k_chunks) {
-      const int s = 8 * l;
-      const uint32_t w = ((g0 >> s) & 255u) | (((g1 >> s) & 255u) << 8) | (((g2 >> s) & 255u) << 16) |
-                         (((g3 >> s) & 255u) << 24);
-      *reinterpret_cast<uint32_t*>(sc + r * 16 + 4 * l) = w;
+      const uint32_t lo = __byte_perm(g0, g1, l | ((l + 4) << 4)), hi = __byte_perm(g2, g3, l | ((l + 4) << 4));
+      *reinterpret_cast<uint32_t*>(sc + r * 16) = __byte_perm(lo, hi, 0x5410);
     }
+  };
+  typename E::Raw a[4], b[4];
+  const int quads = min(4, (min(count, 32) - warp + MQ_WARPS - 1) / MQ_WARPS);   // those with a row
+  if (parts > 1) {
+    if (at.part < quads) {
+      load_quad(at.part, a);
+      finish_quad(at.part, a);
+    }
+    return;
   }
+  if (quads <= 0) return;
+  // The next four rows are on their way while these are worked on.
+  load_quad(0, a);
+  if (quads > 1) load_quad(1, b);
+  finish_quad(0, a);
+  if (quads > 2) load_quad(2, a);
+  if (quads > 1) finish_quad(1, b);
+  if (quads > 3) load_quad(3, b);
+  if (quads > 2) finish_quad(2, a);
+  if (quads > 3) finish_quad(3, b);
 }
 
 // Codes and scales -> values: lane l of a 128-column chunk turns the four code
 // bytes at columns 8 l .. 8 l + 7 into 16 (fp32: 32) bytes.  E2M1 values times
 // a power of two down to 2^-127 are exact in bf16 and fp32.
 template <int kDtype>
-__global__ void __launch_bounds__(MQ_THREADS) mxfp4_dequantize_kernel(const MxDequantParams p, int k_slices) {
+__global__ void __launch_bounds__(MQ_THREADS) mxfp4_dequantize_kernel(const MxDequantParams p, int k_slices, int parts) {
   pdl_wait();
   pdl_launch_dependents();
-  const int block = (int)(blockIdx.x / (unsigned)k_slices), slice = (int)(blockIdx.x - (unsigned)block * k_slices);
+  const Place at = place(k_slices, parts);
+  const int block = at.block, slice = at.slice;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int row0, count;
   if (!find_block(block, p.rows, p.groups, p.offsets, p.dev_status, row0, count)) return;
@@ -194,7 +173,9 @@ __global__ void __launch_bounds__(MQ_THREADS) mxfp4_dequantize_kernel(const MxDe
   const int k = slice * MQ_COLS + half * 128 + 8 * l;
   if (k >= p.K) return;
   const uint8_t* const sc = p.scales + mx_tile_offset(block, k_chunks, slice * 2 + half) + (l >> 2);
-  for (int r = warp; r < 32 && r < count; r += MQ_WARPS) {
+  const int r_step = MQ_WARPS * parts;
+#pragma unroll 2
+  for (int r = warp + MQ_WARPS * at.part; r < 32 && r < count; r += r_step) {
     uint32_t w[4];
     uint32_t b[4];
 #pragma unroll
@@ -239,16 +220,22 @@ __global__ void __launch_bounds__(MQ_THREADS) mxfp4_dequantize_kernel(const MxDe
 // Scale blocks of the rows: those the groups' blocks can reach.
 long long row_blocks(int rows, int groups) { return groups == 0 ? ((long long)rows + 127) / 128 : rows / 128 + groups; }
 
+// With few tiles a warp takes one quad of rows, so that four times as many
+// warps share the latency; with many it takes four and loads ahead.
+constexpr long long MQ_FEW_TILES = 1024;
+
 template <class P, class Kernel>
 cudaError_t launch_rows(const P& p, Kernel kernel, cudaStream_t stream, bool pdl) {
   const int k_slices = (p.K + MQ_COLS - 1) / MQ_COLS;
+  const long long tiles = row_blocks(p.rows, p.groups) * k_slices;
+  const int parts = tiles < MQ_FEW_TILES ? 4 : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(row_blocks(p.rows, p.groups) * k_slices));
+  cfg.gridDim = dim3((unsigned)(tiles * parts));
   cfg.blockDim = dim3(MQ_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   set_pdl(cfg, attr, pdl);
-  return cudaLaunchKernelEx(&cfg, kernel, p, k_slices);
+  return cudaLaunchKernelEx(&cfg, kernel, p, k_slices, parts);
 }
 
 }  // namespace

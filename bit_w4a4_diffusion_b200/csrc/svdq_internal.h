@@ -287,6 +287,12 @@ struct MxGemmParams {
   long long ldy;
   uint8_t* h_codes;       // SwiGLU: [rows, N/2]
   uint8_t* h_scales;      // SwiGLU: tiled, K = N
+  // Narrow kernel with the quantizer inside: x [x_rows, K] of the 16-bit type
+  // instead of codes and scales (t.act and t.sfa unused); null: not.
+  const void* x;
+  long long ldx;
+  const int* row_index;
+  int x_rows;
   int weights_early;      // the weights and offsets were complete before the preceding kernel began
   int splits;             // narrow kernel: CTAs (one cluster) that share a tile's K
   int* dev_status;

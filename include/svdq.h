@@ -440,10 +440,14 @@ int awq_w4a16_linear(int M, int N, int K, const void* x, const void* qweight, co
  * PDL). */
 typedef enum { MXFP4_BF16 = 0, MXFP4_FP16 = 1, MXFP4_FP32 = 2 } mxfp4_dtype;
 #define MXFP4_MAX_GROUPS 512
+/* Up to this many rows the layers quantize x inside the product's kernel. */
+#define MXFP4_FUSED_ROWS 16
+#define MXFP4_FUSED_GROUPED_ROWS 64
 #define SVDQ_DEV_BAD_INDEX 5 /* device status code: offsets or row_index out of range */
 
 /* Sizes in bytes, -1 for unsupported arguments.  groups == 0 in the
- * workspace size: the dense layer. */
+ * workspace size: the dense layer.  mxfp4_workspace_bytes is 0 where the
+ * layer quantizes x inside its product (workspace may be NULL then). */
 long long mxfp4_scale_bytes(int rows, int K);
 long long mxfp4_grouped_scale_bytes(int groups, int rows, int K);
 long long mxfp4_workspace_bytes(int groups, int rows, int K);
@@ -476,7 +480,9 @@ int mxfp4_dequantize(int dtype, int rows, int K, const void* codes, const void* 
  * if they do not overlap in time.
  * The product runs on one of two kernels: 256 x 256 tiles on CTA pairs, or,
  * with few rows per group, a weight stream with the rows as the narrow
- * operand.  SVDQ_MXFP4_GEMM_KERNEL=pair or =narrow in the environment (read
+ * operand; the linear calls with up to MXFP4_FUSED_ROWS (grouped:
+ * MXFP4_FUSED_GROUPED_ROWS) rows are one launch of the latter, with the
+ * quantizer inside.  SVDQ_MXFP4_GEMM_KERNEL=pair or =narrow in the environment (read
  * at every call) forces one; they differ in the order of fp32 sums. */
 int mxfp4_gemm(int dtype, int M, int N, int K, const void* act_codes, const void* act_scales, const void* w_codes,
                const void* w_scales, const void* bias, void* y, long long ldy, int* dev_status, void* stream);

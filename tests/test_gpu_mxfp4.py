@@ -275,6 +275,28 @@ def test_linear_strided_x_and_workspace():
     same_bits(B.mxfp4_linear(x, w, workspace=ws), want)
 
 
+def steps_linear(x, w, bias=None, **kw):
+    """mxfp4_linear in its two steps."""
+    return B.mxfp4_gemm(*B.mxfp4_quantize(x), w, bias=bias, dtype=x.dtype, **kw)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,K", [(8, 32), (136, 96), (1000, 544), (2056, 4096)])
+def test_linear_around_the_fused_limit(N, K, dtype):
+    """Up to 16 rows the product quantizes x itself: the same bits as the two
+    steps, below the limit and above, special values included."""
+    rng = np.random.default_rng(N + K)
+    w = B.to_device(B.mxfp4_pack_weights(F.bf16_bits(rng.standard_normal((N, K)).astype(np.float32))))
+    b = cuda(rng.standard_normal(N).astype(np.float32), dtype)
+    base = C.rows(rng, 40, K + 24, dtype).cuda()
+    base[3, 8] = float("inf")
+    base[5, 20:K] = 0
+    base[6] *= 2.0 ** -18 if dtype == torch.float16 else 2.0 ** -120
+    for M in (1, 2, 7, 8, 9, 15, 16, 17, 40):
+        x = base[:M, 8:8 + K]
+        same_bits(B.mxfp4_linear(x, w, bias=b), steps_linear(x, w, b))
+
+
 # ----------------------------------------------------------------- grouped --
 
 def grouped_case(off, rows, N, K, dtype, seed, matrices=1, pa=-3, pw=-2, pb=-7):
@@ -338,6 +360,53 @@ def test_grouped_linear_gathers(monkeypatch, kernel):
         part = x[idx[off[e]:off[e + 1]].long()]
         same_bits(y[off[e]:off[e + 1]], B.mxfp4_linear(part, we))
     assert (y[230:] == 2.0).all()
+
+
+SMALL = {   # offsets, rows: up to 64 rows the grouped layers quantize x themselves
+    "one row": ([0, 1], 1),
+    "one group": ([0, 64], 64),
+    "all in the last": ([0, 0, 0, 0, 63], 64),
+    "a few each": ([0, 3, 3, 20, 37, 64], 64),
+    "rows of no group": ([5, 6, 40, 41], 50),
+    "above the limit": ([0, 30, 65], 65),
+}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", SMALL)
+@pytest.mark.parametrize("N,K", [(32, 64), (160, 2080)])
+def test_grouped_layers_around_the_fused_limit(name, dtype, N, K):
+    off, rows = SMALL[name]
+    E = len(off) - 1
+    rng = np.random.default_rng(rows + N)
+    x = C.rows(rng, 30, K, dtype).cuda()
+    x[4, 9] = float("nan")
+    offs, idx = cuda(off, torch.int32), cuda(rng.integers(0, 30, rows), torch.int32)
+    w = B.to_device(B.mxfp4_pack_weights(F.bf16_bits(rng.standard_normal((E, N, K)).astype(np.float32) * .1)))
+    up = B.to_device(B.mxfp4_pack_weights(F.bf16_bits(rng.standard_normal((E, 2, N, K)).astype(np.float32) * .1)))
+    down = B.to_device(B.mxfp4_pack_weights(F.bf16_bits(rng.standard_normal((E, K, N)).astype(np.float32) * .1)))
+    b = cuda(rng.standard_normal((E, N)).astype(np.float32), dtype)
+    q = B.mxfp4_quantize(x, offsets=offs, row_index=idx)
+    got, want = (torch.full((rows, N), 6.0, dtype=dtype, device="cuda") for _ in range(2))
+    B.mxfp4_grouped_linear(x, offs, w, row_index=idx, bias=b, y=got)
+    B.mxfp4_grouped_gemm(*q, offs, w, bias=b, dtype=dtype, y=want)
+    same_bits(got, want)
+    got, want = (torch.full((rows, K), 6.0, dtype=dtype, device="cuda") for _ in range(2))
+    B.mxfp4_grouped_mlp_swiglu(x, offs, up, down, row_index=idx, y=got)
+    h = B.mxfp4_grouped_gemm_swiglu_quant(*q, offs, up, dtype=dtype)
+    B.mxfp4_grouped_gemm(*h, offs, down, dtype=dtype, y=want)
+    same_bits(got, want)
+
+
+def test_bad_row_index_in_the_fused_layer():
+    rng = np.random.default_rng(0)
+    x = C.rows(rng, 16, 64, torch.bfloat16).cuda()
+    w, _ = C.weight(rng, (2,), 32, 64, 0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = B.mxfp4_grouped_linear(x, cuda([0, 2, 5], torch.int32), w, row_index=cuda([0, 16, 3, -1, 15], torch.int32),
+                               dev_status=status)
+    assert int(status) == 5
+    assert torch.isnan(y[[1, 3]]).all() and not torch.isnan(y[[0, 2, 4]]).any()
 
 
 # --------------------------------------------------------------------- mlp --

@@ -122,10 +122,26 @@ def test_sizes():
     assert B.mxfp4_scale_bytes(300, 1024, groups=5) == (2 + 5) * 8 * 512
     assert B.mxfp4_scale_bytes(1, 48) == -1 and B.mxfp4_scale_bytes(-1, 32) == -1
     assert B.mxfp4_scale_bytes(1, 32, groups=513) == -1
-    assert B.mxfp4_workspace_bytes(1, 32) == 256 + 512
+    assert B.mxfp4_workspace_bytes(17, 32) == 512 + 512
+    assert B.mxfp4_workspace_bytes(16, 32) == 0 and B.mxfp4_workspace_bytes(64, 32, groups=3) == 0
     assert B.mxfp4_mlp_workspace_bytes(4, 100, 64, 96) == (B.mxfp4_workspace_bytes(100, 64, 4) +
                                                            B.mxfp4_workspace_bytes(100, 96, 4))
+    assert B.mxfp4_mlp_workspace_bytes(4, 8, 64, 96) == 512 + (4 * 512)
     assert B.mxfp4_mlp_workspace_bytes(0, 100, 64, 96) == -1
+
+
+def test_sizes_agree_with_the_library():
+    for rows in (0, 1, 127, 128, 129, 1000):
+        for K in (32, 96, 128, 4128):
+            assert B.mxfp4_scale_bytes(rows, K) == B.lib.mxfp4_scale_bytes(rows, K)
+            for groups in (0, 1, 7, 512, 513, -1):
+                assert B.mxfp4_workspace_bytes(rows, K, groups) == B.lib.mxfp4_workspace_bytes(groups, rows, K)
+                if groups:
+                    assert B.mxfp4_scale_bytes(rows, K, groups) == B.lib.mxfp4_grouped_scale_bytes(groups, rows, K)
+                assert (B.mxfp4_mlp_workspace_bytes(groups, rows, K, 96) ==
+                        B.lib.mxfp4_mlp_workspace_bytes(groups, rows, K, 96))
+    for rows, K in ((-1, 32), (4, 33), (4, 0), (4, -32)):
+        assert B.mxfp4_scale_bytes(rows, K) == B.lib.mxfp4_scale_bytes(rows, K) == -1
 
 
 def test_grouped_blocks_never_meet():
@@ -182,7 +198,7 @@ def test_gemm_refusals(kw, status):
                             a["ldy"], None, None) == status, B.lib.svdq_last_error()
 
 
-def _linear(groups=2, rows=4, N=16, K=64, x=FAKE, ldx=64, idx=None, x_rows=4, off=FAKE, ws=FAKE, ws_bytes=1 << 30,
+def _linear(groups=2, rows=70, N=16, K=64, x=FAKE, ldx=64, idx=None, x_rows=70, off=FAKE, ws=FAKE, ws_bytes=1 << 30,
             dtype=0, y=FAKE, ldy=16):
     return B.lib.mxfp4_grouped_linear(dtype, groups, rows, N, K, x, ldx, idx, x_rows, off, FAKE, FAKE, None, y, ldy,
                                       ws, ws_bytes, None, None)
@@ -190,7 +206,7 @@ def _linear(groups=2, rows=4, N=16, K=64, x=FAKE, ldx=64, idx=None, x_rows=4, of
 
 @pytest.mark.parametrize("kw,status", [
     (dict(groups=0, off=None), 2), (dict(groups=-2), 2), (dict(groups=600), 2), (dict(off=None), 1),
-    (dict(x_rows=3), 1), (dict(ws=None), 1), (dict(ws_bytes=100), 1), (dict(ws=FAKE + 4), 1), (dict(N=4), 2),
+    (dict(x_rows=69), 1), (dict(ws=None), 1), (dict(ws_bytes=100), 1), (dict(ws=FAKE + 4), 1), (dict(N=4), 2),
     (dict(ldx=32), 1), (dict(y=None), 1), (dict(dtype=2), 1), (dict(groups=500, N=1 << 23), 2),
 ])
 def test_grouped_linear_refusals(kw, status):
@@ -198,7 +214,7 @@ def test_grouped_linear_refusals(kw, status):
 
 
 def test_workspace_message():
-    assert B.lib.mxfp4_linear(0, 4, 16, 64, FAKE, 64, FAKE, FAKE, None, FAKE, 16, FAKE, 8, None, None) == 1
+    assert B.lib.mxfp4_linear(0, 40, 16, 64, FAKE, 64, FAKE, FAKE, None, FAKE, 16, FAKE, 8, None, None) == 1
     assert b"workspace" in B.lib.svdq_last_error()
 
 
