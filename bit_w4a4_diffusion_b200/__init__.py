@@ -444,8 +444,8 @@ def awq_w4a16_linear(x, w, bias=None, y=None, stream=None):
 
 MXFP4_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MXFP4_MAX_GROUPS = 512
-MXFP4_FUSED_ROWS = 16
-MXFP4_FUSED_GROUPED_ROWS = 64
+MXFP4_FUSED_ROWS = 4
+MXFP4_FUSED_GROUPED_ROWS = 16
 
 
 def mxfp4_scale_bytes(rows, K, groups=0):

@@ -53,18 +53,31 @@ struct MxRaw32 {
 };
 
 // Eight consecutive elements of a row: how they are loaded, their largest
-// magnitude in an order that integers keep (sign cleared; NaN and infinity on
-// top), and their fp32 values times a power of two.  16-bit magnitudes are
-// compared two at a time as 16-bit integers, which order like the values.
+// magnitude (NaN if there is one), two halves of a word for 16-bit types and
+// in the end as fp32 bits, and their fp32 values times a power of two.
 SVDQ_DEV uint4 mx_load_vec(const void* p, bool reused) {
   const uint4* q = static_cast<const uint4*>(p);
   return reused ? __ldg(q) : __ldcs(q);
 }
-SVDQ_DEV uint32_t mx_top16x2(const uint4& w) {
-  const uint32_t m = 0x7FFF7FFFu;
-  return __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+// The same, issued where it stands: not moved behind a wait to its first use.
+SVDQ_DEV uint4 mx_load_now(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 SVDQ_DEV uint32_t mx_halves_max(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+template <class T2>
+SVDQ_DEV uint32_t mx_max2(uint32_t a, uint32_t b) {   // NaN if either is
+  const T2 m = __hmax2_nan(*reinterpret_cast<const T2*>(&a), *reinterpret_cast<const T2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+template <class T2>
+SVDQ_DEV uint32_t mx_top8(const uint4& w) {
+  const uint32_t m = 0x7FFF7FFFu;
+  return mx_max2<T2>(mx_max2<T2>(w.x & m, w.y & m), mx_max2<T2>(w.z & m, w.w & m));
+}
 
 template <int kDtype>
 struct MxElems;
@@ -74,8 +87,9 @@ struct MxElems<kMxBf16> {
   static constexpr int kSize = 2;
   static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0)}; }
   static SVDQ_DEV Raw load(const uint8_t* x, bool reused) { return {mx_load_vec(x, reused)}; }
-  static SVDQ_DEV uint32_t top(const Raw& r) { return mx_top16x2(r.w); }
-  static SVDQ_DEV uint32_t top_max(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+  static SVDQ_DEV Raw load_now(const uint8_t* x) { return {mx_load_now(x)}; }
+  static SVDQ_DEV uint32_t top(const Raw& r) { return mx_top8<__nv_bfloat162>(r.w); }
+  static SVDQ_DEV uint32_t top_max(uint32_t a, uint32_t b) { return mx_max2<__nv_bfloat162>(a, b); }
   static SVDQ_DEV uint32_t top_bits(uint32_t m) { return mx_halves_max(m) << 16; }
   static SVDQ_DEV void scaled(const Raw& r, float inv, float2 (&v)[4]) {
     const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
@@ -91,8 +105,9 @@ struct MxElems<kMxFp16> {
   static constexpr int kSize = 2;
   static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0)}; }
   static SVDQ_DEV Raw load(const uint8_t* x, bool reused) { return {mx_load_vec(x, reused)}; }
-  static SVDQ_DEV uint32_t top(const Raw& r) { return mx_top16x2(r.w); }
-  static SVDQ_DEV uint32_t top_max(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+  static SVDQ_DEV Raw load_now(const uint8_t* x) { return {mx_load_now(x)}; }
+  static SVDQ_DEV uint32_t top(const Raw& r) { return mx_top8<__half2>(r.w); }
+  static SVDQ_DEV uint32_t top_max(uint32_t a, uint32_t b) { return mx_max2<__half2>(a, b); }
   static SVDQ_DEV uint32_t top_bits(uint32_t m) {
     return __float_as_uint(__half2float(__ushort_as_half((unsigned short)mx_halves_max(m))));
   }

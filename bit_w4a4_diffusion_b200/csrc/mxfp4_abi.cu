@@ -120,18 +120,33 @@ int quantize(const Device& d, int dtype, int rows, int K, const void* x, long lo
 }
 
 // Few enough rows that the narrow kernel quantizes x itself: one launch, no
-// workspace for x.
+// workspace for x.  GPU time of a 4096 x 4096 layer, one kernel / two: 6.0 /
+// 6.9 us at one row, 7.4 / 7.2 at four, 8.8 / 7.2 at eight, and the second
+// launch costs the host 3 us.  Grouped rows count by the largest group, which
+// the host does not know: up to 16 rows are rarely many of one group.
 bool fuses(int groups, int rows) { return rows <= (groups == 0 ? MXFP4_FUSED_ROWS : MXFP4_FUSED_GROUPED_ROWS); }
 
-// Which kernel a product takes; SVDQ_MXFP4_GEMM_KERNEL=pair or =narrow (read
-// at every call) forces one of them.
-bool use_pair(int groups, int rows, int N, int sms) {
+// Row tiles of the narrow kernel: every group's last tile may be short, and a
+// tile has a row.
+long long narrow_m_tiles(int groups, int rows) {
+  return groups == 0 ? ((long long)rows + kMxNarrowRows - 1) / kMxNarrowRows
+                     : std::min<long long>(rows, rows / kMxNarrowRows + (long long)groups);
+}
+
+// Which kernel a product takes.  SVDQ_MXFP4_GEMM_KERNEL=pair or =narrow (read
+// at every call) forces one of them.  Otherwise the narrow kernel while its
+// tiles fit the chip's CTA slots once, or while a group has so few rows on
+// average that the weight bytes dominate.  GPU time narrow / pair, us:
+//   dense, 4096 x 4096: M = 64 6.6 / 10.4, 512 9.9 / 11.0, 768 15.5 / 11.7;
+//   1024 x 4096: 2048 9.8 / 11.0;  12288 x 4096: 192 11.9 / 12.6, 256 17.2 / 12.9
+//   32 groups, 2048 x 2048, rows each: 96 21.9 / 22.2, 128 25.8 / 24.3
+//   SwiGLU, the same: 96 34.9 / 36.4, 128 36.7 / 36.7, 160 44.5 / 36.9
+bool use_pair(int groups, int rows, int N, bool swiglu, int sms) {
   const char* v = getenv("SVDQ_MXFP4_GEMM_KERNEL");
   if (v && strcmp(v, "pair") == 0) return true;
   if (v && strcmp(v, "narrow") == 0) return false;
-  (void)N;
-  (void)sms;
-  return rows / (groups == 0 ? 1 : groups) > 128;
+  if (narrow_m_tiles(groups, rows) * ((N + 127) / 128) <= (long long)kMxNarrowPerSm * sms) return false;
+  return rows / (groups == 0 ? 1 : groups) > (swiglu ? 128 : 96);
 }
 
 // CTAs that share one tile's K: as many as fit the chip once, at most one per
@@ -161,7 +176,7 @@ int product(const Device& d, const Product& g, cudaStream_t stream) {
   const int k_chunks = (g.K + 127) / 128;
   const int groups = g.groups == 0 ? 1 : g.groups;
   const long long matrices = (long long)groups * (g.swiglu ? 2 : 1);
-  const bool pair = g.x == nullptr && use_pair(g.groups, g.rows, g.N, d.sms);
+  const bool pair = g.x == nullptr && use_pair(g.groups, g.rows, g.N, g.swiglu, d.sms);
   MxGemmTmaps t;
   const uint64_t sfa_rows = (uint64_t)scale_blocks(g.groups, g.rows) * k_chunks * 2;
   const uint64_t sfw_rows = (uint64_t)matrices * ((g.N + 127) / 128) * k_chunks * 2;
@@ -204,9 +219,7 @@ int product(const Device& d, const Product& g, cudaStream_t stream) {
   p.dev_status = d.status;
   p.timeout_ns = svdq_get_timeout_ns();
   if (pair) return cuda_status(launch_mxfp4_gemm_pair(p, t, g.swiglu, stream, d.pdl), "mxfp4_gemm_pair launch");
-  const int tile_rows = g.swiglu ? kMxNarrowRowsGlu : kMxNarrowRows;
-  const long long m_tiles = g.groups == 0 ? ((long long)g.rows + tile_rows - 1) / tile_rows
-                                          : std::min<long long>(g.rows, g.rows / tile_rows + (long long)g.groups);
+  const long long m_tiles = narrow_m_tiles(g.groups, g.rows);
   p.splits = choose_splits(m_tiles * ((g.N + 127) / 128), g.K, d.sms);
   return cuda_status(launch_mxfp4_gemm_narrow(p, t, g.swiglu, d.sms, stream, d.pdl), "mxfp4_gemm_narrow launch");
 }

@@ -9,28 +9,32 @@
 // What bounds it: the weight bytes.  A group with m rows does m / 0.53
 // multiply-adds per weight byte, so below some 150 rows HBM is the limit and
 // the kernel is a weight stream: each CTA pulls 128 weight rows x 256 columns
-// (17 KB with their scales) per pipeline stage through TMA into a ring of
-// about 200 KB, which keeps ~30 MB in flight over the chip, and the rows ride
-// along as the narrow operand (N = 16 .. 128, as many as the tile has).
+// (17 KB with their scales) per pipeline stage through TMA, two CTAs to an SM
+// with rings of about 80 KB, which keeps more than 20 MB in flight over the
+// chip, and the rows ride along as the narrow operand (N = 16 .. 64, as many
+// as the tile has).
 // With the weight on the M side a tile of one row costs the tensor core
 // little more than its weight loads; with the rows on the M side (the pair
 // kernel) it would multiply 256 rows of padding.
 //
-// Schedule: tiles are (group, 128 weight rows, up to 128 rows); a persistent
+// Schedule: tiles are (group, 128 weight rows, up to 64 rows); a persistent
 // CTA walks them, its producer running ahead into the next tile while the
-// epilogue drains the last (two accumulators in tensor memory).  With fewer
-// tiles than SMs and no groups to fill them, a cluster of 2, 4 or 8 CTAs
-// shares one tile's K range and adds its partial sums through distributed
-// shared memory, always in rank order.
+// epilogue drains the last.  With fewer tiles than SMs a cluster of 2, 4 or 8
+// CTAs shares one tile's K range and adds its partial sums through
+// distributed shared memory, always in rank order.
 //
-// With a handful of rows the quantizer runs inside (kX): four more warps read
-// x, a K slice each in turn, and write the codes and scale bytes of the row
+// Measured (GPU time of the product): 32 groups of 32 rows, 2048 x 8192: 48.9
+// us, 5.8 TB/s of weights; SwiGLU of them 87.4 us, 6.5 TB/s; 32 x 2048 x 2048
+// 15.7 us, 4.6 TB/s (one CTA per SM with a ring of 200 KB: 17.3).
+//
+// With a handful of rows the quantizer runs inside (kX): one more warp per
+// stage reads x, a K slice at a time, and writes the codes and scale bytes of the row
 // operand straight into the stage, in the layout TMA would have left.  Every
 // tile repeats that work, which is little for few rows, and the layer is one
 // launch instead of two.
 //
 // Roles (6 warps): 0-3 epilogue (tensor-memory lane quarter = warp), 4 TMA
-// producer, 5 MMA issuer; kX: 6-9 quantizer.  Role loops run on whole warps
+// producer, 5 MMA issuer; kX: 6 on, quantizer.  Role loops run on whole warps
 // and issue from one elected lane.  Every mbarrier wait is bounded.
 #include "mxfp4.cuh"
 
@@ -41,36 +45,43 @@ constexpr int BW = 128;                 // weight rows per tile (MMA M)
 constexpr int BK_BYTES = 128;           // 256 elements of K per stage
 constexpr int EPI_WARPS = 4;
 constexpr int PRODUCER_WARP = 4, MMA_WARP = 5;
-constexpr int QUANT_WARP = 6, QUANT_WARPS = 4;
+constexpr int QUANT_WARP = 6;
 constexpr int kNoX = -1;                // kX: x quantized beforehand, or x's dtype
-template <int kX>
-constexpr int num_threads() { return (QUANT_WARP + (kX == kNoX ? 0 : QUANT_WARPS)) * 32; }
 constexpr int MAX_SPLITS = 8;
+constexpr int H_PITCH = 36;             // words: 16-byte reads of eight rows fall into different banks
 constexpr int W_BYTES = BW * BK_BYTES;  // 16 KB
 constexpr int SF_BYTES = 1024;          // 128 rows x 256 columns of scales
 constexpr int BOX_BYTES = kMxNarrowBox * BK_BYTES;
-constexpr int TMEM_COLS = 512;
 constexpr unsigned long long kDrainLimitNs = 2000000000ull;
 
+// Two CTAs share an SM: one's set-up, drain and epilogue pass behind the
+// other's loads, and a dependent kernel finds room before this one ends.
+constexpr int TMEM_COLS = 256;
+constexpr int ROWS = kMxNarrowRows;     // rows per tile (MMA N)
 template <bool kGlu>
 struct Cfg {
-  static constexpr int kWeights = kGlu ? 2 : 1;                            // accumulators per tile
-  static constexpr int kRows = kGlu ? kMxNarrowRowsGlu : kMxNarrowRows;    // rows per tile (MMA N)
-  static constexpr int kStages = kGlu ? 5 : 6;
-  static constexpr int kActBytes = kRows * BK_BYTES;
-  static constexpr int kSfOff = kWeights * W_BYTES + kActBytes;            // SFW (per weight), then SFA
+  static constexpr int kWeights = kGlu ? 2 : 1;                   // weight tiles, and accumulators, per tile
+  static constexpr int kStages = kGlu ? 2 : 3;
+  static constexpr int kBufs = kGlu ? 1 : 2;                      // accumulator buffers
+  static constexpr int kActBytes = ROWS * BK_BYTES;
+  static constexpr int kSfOff = kWeights * W_BYTES + kActBytes;   // SFW (per weight), then SFA
   static constexpr int kStageBytes = kSfOff + (kWeights + 1) * SF_BYTES;
-  static constexpr int kAccCols = kWeights * kRows;                        // per accumulator buffer
+  static constexpr int kAccCols = kWeights * ROWS;                // per accumulator buffer
   static constexpr int kSfCols = 8 * kWeights + 8;
-  static constexpr int kTmemSf = 2 * kAccCols;
-  static constexpr int kStageOutBytes = kGlu ? 0 : 2 * 32 * BW * 2;        // two 32-row output staging buffers
+  static constexpr int kTmemSf = kBufs * kAccCols;
+  // Output staging: two buffers of 32 rows x 128 columns, or (SwiGLU) per
+  // epilogue warp 32 rows x 32 hidden columns of fp32, rows 36 words apart.
+  static constexpr int kStageOutBytes = kGlu ? EPI_WARPS * 32 * H_PITCH * 4 : 2 * 32 * BW * 2;
   static_assert(kStageBytes % 1024 == 0, "stages keep the 1024-byte alignment of SWIZZLE_128B");
   static_assert(kTmemSf + kStages * kSfCols <= TMEM_COLS, "accumulators and scale buffers fit tensor memory");
 };
 
+template <bool kGlu, int kX>
+constexpr int num_threads() { return (QUANT_WARP + (kX == kNoX ? 0 : Cfg<kGlu>::kStages)) * 32; }   // a quantizer warp per stage
+
 struct Ctl {
-  uint64_t full[6];
-  uint64_t empty[6];
+  uint64_t full[4];
+  uint64_t empty[4];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t drain;
@@ -83,9 +94,12 @@ template <bool kGlu>
 constexpr size_t smem_bytes() {
   return 1024 + Cfg<kGlu>::kStages * Cfg<kGlu>::kStageBytes + Cfg<kGlu>::kStageOutBytes + sizeof(Ctl);
 }
-static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "fits the shared memory of one CTA");
-static_assert(kMxNarrowRows * BW * 4 <= Cfg<false>::kStages * Cfg<false>::kStageBytes &&
-                  kMxNarrowRowsGlu * 2 * BW * 4 <= Cfg<true>::kStages * Cfg<true>::kStageBytes,
+// 228 KB per SM, 1 KB of it reserved for each CTA.
+static_assert(kMxNarrowPerSm * (smem_bytes<false>() + 1024) <= 233472 &&
+                  kMxNarrowPerSm * (smem_bytes<true>() + 1024) <= 233472,
+              "two CTAs fit an SM");
+static_assert(ROWS * BW * 4 <= Cfg<false>::kStages * Cfg<false>::kStageBytes &&
+                  ROWS * 2 * BW * 4 <= Cfg<true>::kStages * Cfg<true>::kStageBytes,
               "partial sums reuse the ring");
 
 SVDQ_DEV float4 ld_cluster_f4(uint32_t addr) {
@@ -98,7 +112,7 @@ SVDQ_DEV float4 ld_cluster_f4(uint32_t addr) {
 }
 
 template <bool kGlu, int kX>
-__global__ void __launch_bounds__(num_threads<kX>(), 1)
+__global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     mxfp4_gemm_narrow_kernel(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_w,
                              const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfw,
                              const MxGemmParams p) {
@@ -115,7 +129,7 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
       mbar_init(smem_u32(&ctl->full[s]), kFused ? 2 : 1);   // the producer, and a quantizer warp
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < C::kBufs; ++a) {
       mbar_init(smem_u32(&ctl->acc_full[a]), 1);
       mbar_init(smem_u32(&ctl->acc_empty[a]), EPI_WARPS);
     }
@@ -138,7 +152,7 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
   // Offsets are an input like the weights: with weights_early both were
   // complete before the preceding kernel began.
   if (!p.weights_early) pdl_wait();
-  if (warp == 0) mx_build_sched(&ctl->sched, p.groups, p.offsets, p.rows, C::kRows, p.dev_status);
+  if (warp == 0) mx_build_sched(&ctl->sched, p.groups, p.offsets, p.rows, ROWS, p.dev_status);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -184,12 +198,12 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
       for (int i = 0; i < boxes; ++i)
         tma_load_2d_hint(base + C::kWeights * W_BYTES + i * BOX_BYTES, &tm_act, kb * BK_BYTES,
                          t.row0 + i * kMxNarrowBox, full, pol_a);
-      const int block = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + t.mt * C::kRows / 128;
+      const int block = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + t.mt * ROWS / 128;
       tma_load_2d_hint(base + C::kSfOff + C::kWeights * SF_BYTES, &tm_sfa, 0, (block * k_chunks + 2 * kb) * 2, full,
                        pol_a);
     };
     for (int tile = t_first; tile < num_tiles && ok; tile += t_step) {
-      const MxTile t = mx_decode_tile(sched, tile, tiles_n, C::kRows, e);
+      const MxTile t = mx_decode_tile(sched, tile, tiles_n, ROWS, e);
       const int boxes = (t.rows + kMxNarrowBox - 1) / kMxNarrowBox;
       int kb = kb_begin;
       if (!act_ready) {
@@ -244,14 +258,14 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int tile = t_first; tile < num_tiles && ok; tile += t_step, ++seq) {
-      const MxTile t = mx_decode_tile(sched, tile, tiles_n, C::kRows, e);
-      const int a = seq & 1;
-      if (!mbar_wait_warp(smem_u32(&ctl->acc_empty[a]), ((seq >> 1) & 1) ^ 1, wctx, kDevTimeoutMma)) break;
+      const MxTile t = mx_decode_tile(sched, tile, tiles_n, ROWS, e);
+      const int a = seq % C::kBufs;
+      if (!mbar_wait_warp(smem_u32(&ctl->acc_empty[a]), ((seq / C::kBufs) & 1) ^ 1, wctx, kDevTimeoutMma)) break;
       tc_fence_after();
       const uint32_t n = (uint32_t)((t.rows + 15) & ~15);
       const uint32_t idesc0 = mx_idesc(BW, n, 0), idesc1 = mx_idesc(BW, n, 1);
       // The tile's rows within their 128-row scale block: 32 rows a column.
-      const uint32_t sfa_off = kFused ? 0u : (uint32_t)((t.mt * C::kRows % 128) / 32);
+      const uint32_t sfa_off = kFused ? 0u : (uint32_t)((t.mt * ROWS % 128) / 32);
       for (int kb = kb_begin; kb < kb_end; ++kb) {
         if (!mbar_wait_warp(smem_u32(&ctl->full[stage]), phase, wctx, kDevTimeoutMma)) {
           ok = false;
@@ -279,7 +293,7 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
             if (s < steps) {
 #pragma unroll
               for (int i = 0; i < C::kWeights; ++i)
-                mma_mxfp4(tmem + a * C::kAccCols + i * C::kRows, mx_operand_desc(base + i * W_BYTES + 32 * s),
+                mma_mxfp4(tmem + a * C::kAccCols + i * ROWS, mx_operand_desc(base + i * W_BYTES + 32 * s),
                           mx_operand_desc(sb + 32 * s), s & 1 ? idesc1 : idesc0, sf + 8 * i + 4 * (s >> 1),
                           sf + 8 * C::kWeights + 4 * (s >> 1) + sfa_off, kb > kb_begin || s > 0 ? 1u : 0u);
             }
@@ -304,64 +318,78 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
     mbar_wait(smem_u32(&ctl->drain), 0, drain_ctx, kDevTimeoutDrain);
   } else if (kFused && warp >= QUANT_WARP) {
     // -------------------------------------------------------------- quantizer
-    // Warp w takes every fourth K slice: lane l the eight columns 8 l .. + 7
-    // of the slice, four lanes a block.  x is read while the stage is still
-    // in use; a slice's rows come eight at a time.
+    // Warp w fills stage w: lane l the eight columns 8 l .. + 7 of a slice,
+    // four lanes a block.  The loads of a slice's first eight rows go out
+    // together while the stage is still in use.  (One warp per stage, so that
+    // each sees every phase of the one barrier that it waits on: with the
+    // slices dealt out otherwise a warp could come to a barrier two phases
+    // early, where its parity looks like that of the phase it wants.)
     if constexpr (kFused) {
       using E = MxElems<kX>;
-      const int l8 = 8 * lane;
+      const int stage = warp - QUANT_WARP;
+      uint8_t* const act = smem + stage * C::kStageBytes + C::kWeights * W_BYTES;
+      uint8_t* const sf = smem + stage * C::kStageBytes + C::kSfOff + C::kWeights * SF_BYTES + (lane >> 4) * 512 +
+                          ((lane >> 2) & 3);
+      // Rows r .. r + N - 1 of the tile, their chains side by side.
+      auto store_rows = [&](int r, uint32_t lost, const auto& raw) {
+        constexpr int N = sizeof(raw) / sizeof(raw[0]);
+        uint32_t m[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) m[i] = E::top(raw[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) m[i] = E::top_max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+#pragma unroll
+        for (int i = 0; i < N; ++i) m[i] = E::top_max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t b = (lost >> i) & 1u ? 255u : mx_scale_byte(E::top_bits(m[i]));
+          float2 v[4];
+          E::scaled(raw[i], mx_inv_scale(b), v);
+          // 128-byte rows, 16-byte chunks XOR-ed by the row: SWIZZLE_128B.
+          // Columns past K were read as zeros: codes and byte 0.
+          *reinterpret_cast<uint32_t*>(act + (r + i) * 128 + (((lane >> 2) ^ ((r + i) & 7)) << 4) + (lane & 3) * 4) =
+              b == 255u ? 0u : mx_e2m1x8(v);
+          if ((lane & 3) == 0) sf[((r + i) & 31) * 16 + ((r + i) >> 5) * 4] = (uint8_t)b;
+        }
+      };
+      using Raw = typename E::Raw;
       int count = 0, e = 0;    // slices of all tiles so far
       bool ok = true;
       for (int tile = t_first; tile < num_tiles && ok; tile += t_step) {
-        const MxTile t = mx_decode_tile(sched, tile, tiles_n, C::kRows, e);
-        for (int kb = kb_begin; kb < kb_end; ++kb, ++count) {
-          if ((count & (QUANT_WARPS - 1)) != warp - QUANT_WARP) continue;
-          const int stage = count % C::kStages;
+        const MxTile t = mx_decode_tile(sched, tile, tiles_n, ROWS, e);
+        for (int kb = kb_begin; kb < kb_end && ok; ++kb, ++count) {
+          if (count % C::kStages != stage) continue;
           const uint32_t phase = (uint32_t)(count / C::kStages) & 1;
-          const int k = kb * 256 + l8;
-          const bool k_ok = k < p.K;
-          uint8_t* const act = smem + stage * C::kStageBytes + C::kWeights * W_BYTES;
-          uint8_t* const sf = smem + stage * C::kStageBytes + C::kSfOff + C::kWeights * SF_BYTES +
-                              (lane >> 4) * 512 + ((lane >> 2) & 3);
-          bool waited = false;
+          const int k = kb * 256 + 8 * lane;
+          const uint8_t* const x = static_cast<const uint8_t*>(p.x) + (size_t)k * E::kSize;
           for (int r0 = 0; r0 < t.rows; r0 += 8) {
-            typename E::Raw raw[8];
-            uint32_t lost = 0;
+            const int n = min(t.rows - r0, 8);
+            Raw raw[8];
+            uint32_t lost = 0;      // rows whose index is out of range
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               raw[i] = E::zero();
-              if (r0 + i < t.rows) {
+              if (i < n) {
                 int src = t.row0 + r0 + i;
                 if (p.row_index != nullptr) {
                   src = __ldg(p.row_index + src);
                   if (src < 0 || src >= p.x_rows) lost |= 1u << i;
                 }
-                if (k_ok && !((lost >> i) & 1u))
-                  raw[i] = E::load(static_cast<const uint8_t*>(p.x) + ((size_t)src * p.ldx + k) * E::kSize, true);
+                if (k < p.K && !((lost >> i) & 1u)) raw[i] = E::load_now(x + (size_t)src * p.ldx * E::kSize);
               }
             }
             if (lost && p.dev_status) atomicCAS(p.dev_status, 0, kDevBadIndex);
-            if (!waited) {
-              if (!mbar_wait_warp(smem_u32(&ctl->empty[stage]), phase ^ 1, wctx, kDevTimeoutProducer)) {
-                ok = false;
-                break;
-              }
-              waited = true;
+            if (r0 == 0 && !mbar_wait_warp(smem_u32(&ctl->empty[stage]), phase ^ 1, wctx, kDevTimeoutProducer)) {
+              ok = false;
+              break;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = r0 + i;
-              if (r >= t.rows) break;
-              uint32_t m = E::top(raw[i]);
-              m = E::top_max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-              m = E::top_max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-              const uint32_t b = (lost >> i) & 1u ? 255u : mx_scale_byte(E::top_bits(m));
-              float2 v[4];
-              E::scaled(raw[i], mx_inv_scale(b), v);
-              // 128-byte rows, 16-byte chunks XOR-ed by the row: SWIZZLE_128B.
-              *reinterpret_cast<uint32_t*>(act + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) =
-                  b == 255u ? 0u : mx_e2m1x8(v);
-              if ((lane & 3) == 0) sf[(r & 31) * 16 + (r >> 5) * 4] = k_ok ? (uint8_t)b : (uint8_t)0;
+            if (n == 1) {
+              store_rows(r0, lost, reinterpret_cast<const Raw(&)[1]>(raw[0]));
+            } else if (n == 2) {
+              store_rows(r0, lost, reinterpret_cast<const Raw(&)[2]>(raw[0]));
+            } else {        // up to three rows of zeros behind the tile's last are its own padding
+              store_rows(r0, lost, reinterpret_cast<const Raw(&)[4]>(raw[0]));
+              if (n > 4) store_rows(r0 + 4, lost >> 4, reinterpret_cast<const Raw(&)[4]>(raw[4]));
             }
           }
           if (!ok) break;
@@ -378,15 +406,15 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
     const bool fp16 = p.fp16 != 0;
     int e = 0, seq = 0, out_seq = 0;
     for (int tile = t_first; tile < num_tiles; tile += t_step, ++seq) {
-      const MxTile t = mx_decode_tile(sched, tile, tiles_n, C::kRows, e);
-      const int a = seq & 1;
+      const MxTile t = mx_decode_tile(sched, tile, tiles_n, ROWS, e);
+      const int a = seq % C::kBufs;
       const int n0 = t.nt * BW, n = n0 + 32 * q + lane;
       float b0 = 0.f, b1 = 0.f;
       if (p.bias != nullptr && n < p.N && splits == 1) {
         b0 = mx_load16(p.bias + (size_t)t.e * C::kWeights * p.N + n, fp16);
         if constexpr (kGlu) b1 = mx_load16(p.bias + ((size_t)t.e * 2 + 1) * p.N + n, fp16);
       }
-      const bool got = mbar_wait(smem_u32(&ctl->acc_full[a]), (seq >> 1) & 1, wctx, kDevTimeoutEpilogue);
+      const bool got = mbar_wait(smem_u32(&ctl->acc_full[a]), (seq / C::kBufs) & 1, wctx, kDevTimeoutEpilogue);
       if (named_bar_any(2, EPI_WARPS * 32, !got)) break;   // decided by all four warps
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * C::kAccCols);
@@ -396,7 +424,7 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
         tmem_ld_32x32b_x32(acc + 32 * c, r);
         if constexpr (kGlu) {
           uint32_t r2[32];
-          tmem_ld_32x32b_x32(acc + C::kRows + 32 * c, r2);
+          tmem_ld_32x32b_x32(acc + ROWS + 32 * c, r2);
           tmem_ld_wait(r);
           reg_fence(r2);
           if (c == chunks - 1) {
@@ -417,40 +445,42 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
           // 32 lanes = one block of 32 hidden columns (N % 32 == 0: a warp
           // lies inside N or is padding of the last scale tile).
           const bool in_n = n0 + 32 * q < p.N;
-          const int local = t.mt * C::kRows + 32 * c;   // row within the group
+          const int local = t.mt * ROWS + 32 * c;   // row within the group
           const int nblk = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + local / 128;
           uint8_t* const sc = p.h_scales + mx_tile_offset(nblk, tiles_n, t.nt) + (local % 128) / 32 * 4 + q;
           uint8_t* const codes = p.h_codes + (size_t)(t.row0 + 32 * c) * (p.N / 2) + (n0 + 32 * q) / 2;
+          // h goes through shared memory, so that a lane then holds a row's
+          // whole block: its maximum, scale and codes need no other lane.
+          float* const hbuf = reinterpret_cast<float*>(out_base) + q * 32 * H_PITCH;
+          __syncwarp();   // the reads of the chunk before are done
 #pragma unroll
-          for (int j8 = 0; j8 < 32; j8 += 8) {
-            if (32 * c + j8 >= t.rows) break;
-            uint32_t word = 0, byte = 0;   // lane l: codes (its quarter) and scale of row j8 + l % 8
+          for (int j = 0; j < 32; ++j)
+            hbuf[j * H_PITCH + lane] =
+                mx_swiglu(__fadd_rn(__uint_as_float(r[j]), b0), __fadd_rn(__uint_as_float(r2[j]), b1));
+          __syncwarp();
+          if (32 * c + lane < t.rows) {
+            const float4* const hrow = reinterpret_cast<const float4*>(hbuf + lane * H_PITCH);
+            float4 h[8];
+            uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float h = mx_swiglu(__fadd_rn(__uint_as_float(r[j8 + j]), b0),
-                                        __fadd_rn(__uint_as_float(r2[j8 + j]), b1));
-              const uint32_t t_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu);
-              const uint32_t sb = mx_scale_byte(t_bits);
-              const float v = __fmul_rn(h, mx_inv_scale(sb));
-              uint32_t code;
-              asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n\t"
-                  "mov.b32 %0, {x, x, x, x};\n\t}"
-                  : "=r"(code)
-                  : "f"(v), "f"(0.0f));
-              code = sb == 255u ? 0u : (code & 15u) << (4 * (lane & 7));
-              code |= __shfl_xor_sync(0xffffffffu, code, 1);
-              code |= __shfl_xor_sync(0xffffffffu, code, 2);
-              code |= __shfl_xor_sync(0xffffffffu, code, 4);
-              if ((lane & 7) == j) {
-                word = code;
-                byte = sb;
-              }
+              h[j] = hrow[j];
+              top = max(top, max(max(__float_as_uint(h[j].x) & 0x7FFFFFFFu, __float_as_uint(h[j].y) & 0x7FFFFFFFu),
+                                 max(__float_as_uint(h[j].z) & 0x7FFFFFFFu, __float_as_uint(h[j].w) & 0x7FFFFFFFu)));
             }
-            const int j = j8 + (lane & 7);
-            if (32 * c + j < t.rows) {
-              if (in_n) *reinterpret_cast<uint32_t*>(codes + (size_t)j * (p.N / 2) + 4 * (lane >> 3)) = word;
-              if (lane < 8) sc[j * 16] = in_n ? (uint8_t)byte : (uint8_t)0;
+            const uint32_t sb = mx_scale_byte(top);
+            const float2 inv = make_float2(mx_inv_scale(sb), mx_inv_scale(sb));
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 v[4] = {__fmul2_rn(make_float2(h[2 * j].x, h[2 * j].y), inv),
+                                   __fmul2_rn(make_float2(h[2 * j].z, h[2 * j].w), inv),
+                                   __fmul2_rn(make_float2(h[2 * j + 1].x, h[2 * j + 1].y), inv),
+                                   __fmul2_rn(make_float2(h[2 * j + 1].z, h[2 * j + 1].w), inv)};
+              w[j] = sb == 255u ? 0u : mx_e2m1x8(v);
             }
+            if (in_n) *reinterpret_cast<uint4*>(codes + (size_t)lane * (p.N / 2)) = make_uint4(w[0], w[1], w[2], w[3]);
+            sc[lane * 16] = in_n ? (uint8_t)sb : (uint8_t)0;
           }
         } else {
           tmem_ld_wait(r);
@@ -499,7 +529,7 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
     cluster_sync();
     if (t_first < num_tiles) {
       int e = 0;
-      const MxTile t = mx_decode_tile(sched, t_first, tiles_n, C::kRows, e);
+      const MxTile t = mx_decode_tile(sched, t_first, tiles_n, ROWS, e);
       const bool fp16 = p.fp16 != 0;
       const int n = t.nt * BW + 4 * lane;
       const bool in_n = n < p.N;          // N is a multiple of 8 (SwiGLU: 32)
@@ -511,7 +541,7 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
           bias[w][i] = p.bias != nullptr && in_n
                            ? mx_load16(p.bias + ((size_t)t.e * C::kWeights + w) * p.N + n + i, fp16)
                            : 0.f;
-      for (int j = (int)rank + splits * warp; j < t.rows; j += splits * (num_threads<kX>() / 32)) {
+      for (int j = (int)rank + splits * warp; j < t.rows; j += splits * (num_threads<kGlu, kX>() / 32)) {
         float v[C::kWeights][4];
 #pragma unroll
         for (int w = 0; w < C::kWeights; ++w) {
@@ -549,7 +579,7 @@ __global__ void __launch_bounds__(num_threads<kX>(), 1)
                                 make_float2(__fmul_rn(h[2], inv), __fmul_rn(h[3], inv)), make_float2(0.f, 0.f),
                                 make_float2(0.f, 0.f)};
           const uint32_t code = sb == 255u ? 0u : mx_e2m1x8(v2);
-          const int local = t.mt * C::kRows + j;   // row within the group
+          const int local = t.mt * ROWS + j;   // row within the group
           const int block = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + local / 128;
           if (in_n)
             *reinterpret_cast<uint16_t*>(p.h_codes + (size_t)(t.row0 + j) * (p.N / 2) + n / 2) = (uint16_t)code;
@@ -580,12 +610,12 @@ cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, int num_sms
   if (cudaError_t e = mx_allow_smem<mxfp4_gemm_narrow_kernel<kGlu, kX>>(smem)) return e;
   // As many tiles as the rows can make: every group's last tile may be short.
   const long long groups = p.groups == 0 ? 1 : p.groups;
-  const long long by_rows = (long long)(p.rows + C::kRows - 1) / C::kRows;
-  const long long m_tiles = p.groups == 0 ? by_rows : std::min<long long>(p.rows, p.rows / C::kRows + groups);
+  const long long by_rows = (long long)(p.rows + ROWS - 1) / ROWS;
+  const long long m_tiles = p.groups == 0 ? by_rows : std::min<long long>(p.rows, p.rows / ROWS + groups);
   const long long tiles = m_tiles * ((p.N + BW - 1) / BW);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.splits > 1 ? tiles * p.splits : std::min<long long>(tiles, num_sms)));
-  cfg.blockDim = dim3(num_threads<kX>());
+  cfg.gridDim = dim3((unsigned)(p.splits > 1 ? tiles * p.splits : std::min<long long>(tiles, (long long)kMxNarrowPerSm * num_sms)));
+  cfg.blockDim = dim3(num_threads<kGlu, kX>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

@@ -7,30 +7,56 @@
 // nothing is read twice, so HBM bounds them (2.53 bytes per element for 16-bit
 // data) once there are enough rows, and the launch below that.
 //
-// Mapping: a CTA owns one 128-row scale block x 256 columns.  A warp takes
-// the four rows r, r + 32, r + 64, r + 96 of it, whose scale bytes for four
-// neighbouring groups are 16 consecutive bytes of the tiled layout: its lanes
-// read 16 bytes (eight 16-bit elements) of each row, so a row's load and its
-// 128-byte code store are contiguous across the warp, four lanes share a
-// block's maximum by two shuffles, and a 4 x 4 byte exchange among the lanes
-// of a 128-column chunk turns their scales into four aligned words.
+// Mapping: a warp's unit of work is four rows r, r + 32, r + 64, r + 96 of a
+// 128-row scale block by 256 columns: 32 blocks, one per lane (lane 8 i + g:
+// block g of row r + 32 i), so that a lane finds its block's maximum and scale
+// without the others.  Memory sees whole rows all the same: the quantizer
+// copies the unit to shared memory with cp.async, 512 contiguous bytes of a
+// row per instruction (rows may come from anywhere, so a gather costs
+// nothing), and reads blocks back from there; the 16-byte chunks of a row are
+// permuted so that both sides are free of bank conflicts.  All units of a
+// warp are on their way before the first is worked on.  A unit's 32 scale
+// bytes are two 16-byte runs of the tiled layout.  The inverse takes the same
+// way back: 16 bytes of codes per lane, values through shared memory, a row's
+// 512 bytes out by one bulk copy.
+//
+// Measured (GPU time; a device copy runs at 6.49 TB/s in the same harness):
+// quantize 16384 x 8192 bf16 49.7 us, 6.83 TB/s; fp32 86.2 us, 7.05 TB/s;
+// 1001 x 4096 3.1 us; 32768 rows x 2048 gathered from 8192 30.9 us, 5.5 TB/s
+// of L2 and HBM traffic.  Dequantize 16384 x 8192 to bf16 53.6 us, 6.33 TB/s.
+// With the block's maximum taken by shuffles between four lanes of 8 elements
+// each, and no staging, the quantizer took 59.3 us: about 90 instructions per
+// 8 elements, issue slots the limit, against about 40 here.
 #include "mxfp4.cuh"
 
 namespace svdq {
 namespace {
 
-constexpr int MQ_WARPS = 8;
-constexpr int MQ_THREADS = MQ_WARPS * 32;
-constexpr int MQ_COLS = 256;
+constexpr int MQ_COLS = 256;                    // columns of a unit
+// Units of a warp, unless the launch spreads them.  Two against four: 4096 x
+// 4096 8.7 us (9.1), 16384 x 8192 49.7 (50.2), gathered rows 30.9 (29.6).
+constexpr int MQ_UNITS = 2;
+// Warps per CTA: 32 KB of staging for the quantizer either way.
+template <int kDtype>
+constexpr int quant_warps() { return kDtype == kMxFp32 ? 4 : 8; }
+template <int kDtype>
+constexpr int unit_bytes() { return 4 * MQ_COLS * (kDtype == kMxFp32 ? 4 : 2); }
 
-// A CTA's scale block and column slice; with parts = 4 it has one of the four
-// row quads of each warp instead of all four.
+// A warp's scale block and column slice, and its row quads first, first +
+// step, ...: quad t are the rows t, t + 32, t + 64, t + 96.  With `spread` a
+// warp has one quad instead of MQ_UNITS.
 struct Place {
-  int block, slice, part;
+  int block, slice, first, step;
 };
-SVDQ_DEV Place place(int k_slices, int parts) {
-  const unsigned tile = blockIdx.x / (unsigned)parts, block = tile / (unsigned)k_slices;
-  return {(int)block, (int)(tile - block * k_slices), (int)(blockIdx.x - tile * parts)};
+template <int kWarps>
+SVDQ_DEV Place place(int k_slices, int spread) {
+  // CTAs of one tile (scale block x slice): 32 quads / (warps x quads each).
+  constexpr unsigned kParts = 32 / (kWarps * MQ_UNITS);
+  const unsigned parts = spread ? kParts * MQ_UNITS : kParts;
+  const unsigned tile = blockIdx.x / parts, part = blockIdx.x - tile * parts;
+  const unsigned block = tile / (unsigned)k_slices;
+  return {(int)block, (int)(tile - block * k_slices), (int)(part * kWarps + (threadIdx.x >> 5)),
+          (int)(parts * kWarps)};
 }
 
 // The rows of scale block `block`: first row, how many (at most 128), and
@@ -63,33 +89,64 @@ SVDQ_DEV bool find_block(int block, int rows, int groups, const int* offsets, in
   return true;
 }
 
+SVDQ_DEV void cp_async16(uint32_t dst, const void* src, bool take) {
+  // Bytes not taken are zero-filled.
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+SVDQ_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+SVDQ_DEV void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+SVDQ_DEV uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+SVDQ_DEV void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+SVDQ_DEV void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                   reinterpret_cast<uint64_t>(dst)),
+               "r"(src), "r"(bytes)
+               : "memory");
+}
+
 template <int kDtype>
-__global__ void __launch_bounds__(MQ_THREADS) mxfp4_quantize_kernel(const MxQuantParams p, int k_slices, int parts) {
+__global__ void __launch_bounds__(quant_warps<kDtype>() * 32) mxfp4_quantize_kernel(const MxQuantParams p, int k_slices,
+                                                                                   int spread) {
   using E = MxElems<kDtype>;
+  constexpr int kWarps = quant_warps<kDtype>(), kUnit = unit_bytes<kDtype>();
+  constexpr int kChunks = 32 * E::kSize / 16;           // 16-byte chunks of a block: 4 or 8
+  extern __shared__ __align__(128) uint8_t staging[];
   pdl_wait();
   // Every CTA of this grid has begun by the time a dependent kernel starts.
   pdl_launch_dependents();
-  const Place at = place(k_slices, parts);
-  const int block = at.block, slice = at.slice;
+  const Place at = place<kWarps>(k_slices, spread);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int row0, count;
-  if (!find_block(block, p.rows, p.groups, p.offsets, p.dev_status, row0, count)) return;
+  if (!find_block(at.block, p.rows, p.groups, p.offsets, p.dev_status, row0, count)) return;
+  const int quads_left = min(count, 32) - at.first;     // those with a row, from this warp's first on
+  if (quads_left <= 0) return;
+  const int units = spread ? 1 : min(MQ_UNITS, (quads_left + at.step - 1) / at.step);
 
-  const int k_chunks = (p.K + 127) / 128;
-  const int half = lane >> 4, l = lane & 15;            // 128-column chunk and the lane's place in it
-  const int k = slice * MQ_COLS + half * 128 + 8 * l;
-  const bool k_ok = k < p.K;                            // uniform over a block's four lanes
-  const int chunk = slice * 2 + half;
-  uint8_t* const sc = p.scales + mx_tile_offset(block, k_chunks, chunk) + 4 * l;
-  const uint8_t* const x = static_cast<const uint8_t*>(p.x) + (size_t)k * E::kSize;
+  const int k0 = at.slice * MQ_COLS;
+  const uint32_t base = smem_u32(staging) + (uint32_t)(warp * (spread ? 1 : MQ_UNITS) * kUnit);
   const size_t pitch = (size_t)p.ldx * E::kSize;
+  const uint8_t* const x = static_cast<const uint8_t*>(p.x) + (size_t)k0 * E::kSize;
+  const uint32_t row_bytes = (uint32_t)min(p.K - k0, MQ_COLS) * E::kSize;
   const bool gather = p.row_index != nullptr;
 
-  // The warp's rows are warp + 8 t + 32 i for t, i < 4; lane 4 t + i holds
-  // where row (t, i) comes from: -1 past the block's rows, -2 out of range.
+  // Lane 4 t + i holds where row at.first + t step + 32 i comes from: -1 past
+  // the block's rows, -2 out of range.
   int src = -1;
   {
-    const int rr = warp + MQ_WARPS * (l >> 2) + 32 * (l & 3);
+    const int rr = at.first + at.step * ((lane >> 2) % MQ_UNITS) + 32 * (lane & 3);
     if (rr < count) {
       src = row0 + rr;
       if (gather) {
@@ -101,156 +158,209 @@ __global__ void __launch_bounds__(MQ_THREADS) mxfp4_quantize_kernel(const MxQuan
       }
     }
   }
-  auto load_quad = [&](int t, typename E::Raw (&raw)[4]) {
+  // Chunk q of a row lies at chunk q ^ (what tells the blocks apart that share
+  // its banks): 16-bit, blocks g and g + 2; fp32, every block.
+  auto swizzle = [](int q) { return kChunks == 4 ? q ^ ((q >> 3) & 3) : q ^ ((q >> 3) & 7); };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = __shfl_sync(0xffffffffu, src, 4 * t + i);
-      raw[i] = s >= 0 && k_ok ? E::load(x + (size_t)s * pitch, gather) : E::zero();
-    }
-  };
-  auto finish_quad = [&](int t, const typename E::Raw (&raw)[4]) {
-    const int r = warp + MQ_WARPS * t;
-    uint32_t mine = 0;                                  // byte i: the scale of row r + 32 i, this lane's block
+  for (int t = 0; t < MQ_UNITS; ++t) {
+    if (t < units) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int s = __shfl_sync(0xffffffffu, src, 4 * t + i);
-      if (s == -1) continue;                            // the same in every lane
-      uint32_t m = E::top(raw[i]);
-      m = E::top_max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = E::top_max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const uint32_t b = s == -2 ? 255u : mx_scale_byte(E::top_bits(m));
-      float2 v[4];
-      E::scaled(raw[i], mx_inv_scale(b), v);
-      const uint32_t w = b == 255u ? 0u : mx_e2m1x8(v);
-      mine |= (k_ok ? b : 0u) << (8 * i);
-      if (k_ok)
-        *reinterpret_cast<uint32_t*>(p.codes + (size_t)(row0 + r + 32 * i) * (p.K / 2) + k / 2) = w;
-    }
-    // Lanes 0..3 of the chunk collect one row's four group bytes each.
-    const uint32_t g0 = __shfl_sync(0xffffffffu, mine, half * 16), g1 = __shfl_sync(0xffffffffu, mine, half * 16 + 4),
-                   g2 = __shfl_sync(0xffffffffu, mine, half * 16 + 8),
-                   g3 = __shfl_sync(0xffffffffu, mine, half * 16 + 12);
-    if (l < 4 && chunk < k_chunks) {
-      const uint32_t lo = __byte_perm(g0, g1, l | ((l + 4) << 4)), hi = __byte_perm(g2, g3, l | ((l + 4) << 4));
-      *reinterpret_cast<uint32_t*>(sc + r * 16) = __byte_perm(lo, hi, 0x5410);
-    }
-  };
-  typename E::Raw a[4], b[4];
-  const int quads = min(4, (min(count, 32) - warp + MQ_WARPS - 1) / MQ_WARPS);   // those with a row
-  if (parts > 1) {
-    if (at.part < quads) {
-      load_quad(at.part, a);
-      finish_quad(at.part, a);
-    }
-    return;
-  }
-  if (quads <= 0) return;
-  // The next four rows are on their way while these are worked on.
-  load_quad(0, a);
-  if (quads > 1) load_quad(1, b);
-  finish_quad(0, a);
-  if (quads > 2) load_quad(2, a);
-  if (quads > 1) finish_quad(1, b);
-  if (quads > 3) load_quad(3, b);
-  if (quads > 2) finish_quad(2, a);
-  if (quads > 3) finish_quad(3, b);
-}
-
-// Codes and scales -> values: lane l of a 128-column chunk turns the four code
-// bytes at columns 8 l .. 8 l + 7 into 16 (fp32: 32) bytes.  E2M1 values times
-// a power of two down to 2^-127 are exact in bf16 and fp32.
-template <int kDtype>
-__global__ void __launch_bounds__(MQ_THREADS) mxfp4_dequantize_kernel(const MxDequantParams p, int k_slices, int parts) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const Place at = place(k_slices, parts);
-  const int block = at.block, slice = at.slice;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int row0, count;
-  if (!find_block(block, p.rows, p.groups, p.offsets, p.dev_status, row0, count)) return;
-  const int k_chunks = (p.K + 127) / 128;
-  const int half = lane >> 4, l = lane & 15;
-  const int k = slice * MQ_COLS + half * 128 + 8 * l;
-  if (k >= p.K) return;
-  const uint8_t* const sc = p.scales + mx_tile_offset(block, k_chunks, slice * 2 + half) + (l >> 2);
-  const int r_step = MQ_WARPS * parts;
-#pragma unroll 2
-  for (int r = warp + MQ_WARPS * at.part; r < 32 && r < count; r += r_step) {
-    uint32_t w[4];
-    uint32_t b[4];
+      for (int i = 0; i < 4; ++i) {
+        const int s = __shfl_sync(0xffffffffu, src, 4 * t + i);
+        const uint8_t* const row = x + (s >= 0 ? (size_t)s * pitch : 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = b[i] = 0;
-      if (r + 32 * i < count) {
-        w[i] = __ldg(reinterpret_cast<const uint32_t*>(p.codes + (size_t)(row0 + r + 32 * i) * (p.K / 2) + k / 2));
-        b[i] = __ldg(sc + r * 16 + 4 * i);
+        for (int h = 0; h < kChunks / 4; ++h) {
+          const int q = 32 * h + lane;
+          const bool take = s >= 0 && (uint32_t)(16 * q) < row_bytes;
+          cp_async16(base + t * kUnit + i * (kUnit / 4) + 16 * swizzle(q), take ? row + 16 * q : x, take);
+        }
       }
     }
+    cp_async_commit();
+  }
+
+  const int i = lane >> 3, g = lane & 7;                // this lane's row of a unit, and its block
+  const int k_chunks = (p.K + 127) / 128;
+  const int chunk = at.slice * 2 + (g >> 2);
+  const bool g_ok = k0 + 32 * g < p.K;
+  uint8_t* const codes = p.codes + (size_t)(row0 + 32 * i) * (p.K / 2) + k0 / 2 + 16 * g;
+  uint8_t* const sc = p.scales + mx_tile_offset(at.block, k_chunks, chunk) + 4 * i;
+  auto finish = [&](int t) {
+    __syncwarp();                                       // every lane's copies of the unit have landed
+    const int r = at.first + t * at.step;
+    typename E::Raw raw[4];                             // 8 elements each
+    const uint32_t row = base + t * kUnit + i * (kUnit / 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (r + 32 * i >= count) continue;
-      // 2^(b - 127): b = 0 is the subnormal 2^-127, 255 is NaN.
-      const float scale = __uint_as_float(b[i] == 255u ? 0x7FC00000u : b[i] == 0u ? 0x00400000u : b[i] << 23);
-      float v[8];
+    for (int c = 0; c < 4; ++c) {
+      if constexpr (kChunks == 4)
+        raw[c] = {lds128(row + 16 * swizzle(4 * g + c))};
+      else
+        raw[c] = {lds128(row + 16 * swizzle(8 * g + 2 * c)), lds128(row + 16 * swizzle(8 * g + 2 * c + 1))};
+    }
+    const uint32_t m = E::top_max(E::top_max(E::top(raw[0]), E::top(raw[1])),
+                                  E::top_max(E::top(raw[2]), E::top(raw[3])));
+    uint32_t b = mx_scale_byte(E::top_bits(m));
+    if (gather && __shfl_sync(0xffffffffu, src, 4 * t + i) == -2) b = 255u;
+    const float inv = mx_inv_scale(b);
+    uint32_t w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float2 v[4];
+      E::scaled(raw[c], inv, v);
+      w[c] = b == 255u ? 0u : mx_e2m1x8(v);
+    }
+    if (g_ok && r + 32 * i < count)
+      *reinterpret_cast<uint4*>(codes + (size_t)r * (p.K / 2)) = make_uint4(w[0], w[1], w[2], w[3]);
+    // Four lanes' bytes to one word of the scale tile (columns past K and
+    // rows past the last were read as zeros: byte 0).
+    uint32_t word = b << (8 * (g & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2);
+    if ((g & 3) == 0 && chunk < k_chunks) *reinterpret_cast<uint32_t*>(sc + r * 16) = word;
+  };
+  cp_async_wait<1>();
+  finish(0);
+  if (units > 1) {
+    cp_async_wait<0>();
+    finish(1);
+  }
+}
+
+// Codes and scales -> values.  E2M1 values times a power of two down to 2^-127
+// are exact in bf16 and fp32.
+template <int kDtype>
+__global__ void __launch_bounds__(8 * 32) mxfp4_dequantize_kernel(const MxDequantParams p, int k_slices, int spread) {
+  constexpr int kSize = kDtype == kMxFp32 ? 4 : 2;
+  constexpr int kUnit = unit_bytes<kDtype>();
+  extern __shared__ __align__(128) uint8_t staging[];
+  pdl_wait();
+  pdl_launch_dependents();
+  const Place at = place<8>(k_slices, spread);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int row0, count;
+  if (!find_block(at.block, p.rows, p.groups, p.offsets, p.dev_status, row0, count)) return;
+  const int quads_left = min(count, 32) - at.first;
+  if (quads_left <= 0) return;
+  const int units = spread ? 1 : min(MQ_UNITS, (quads_left + at.step - 1) / at.step);
+
+  const int k0 = at.slice * MQ_COLS, k_chunks = (p.K + 127) / 128;
+  const int i = lane >> 3, g = lane & 7;
+  const bool g_ok = k0 + 32 * g < p.K;
+  const uint8_t* const codes = p.codes + (size_t)(row0 + 32 * i) * (p.K / 2) + k0 / 2 + 16 * g;
+  const uint8_t* const sc =
+      p.scales + mx_tile_offset(at.block, k_chunks, at.slice * 2 + (g >> 2)) + 4 * i + (g & 3);
+  const uint32_t row_bytes = (uint32_t)min(p.K - k0, MQ_COLS) * kSize;
+  uint4 w[MQ_UNITS];
+  uint32_t b[MQ_UNITS];
+#pragma unroll
+  for (int t = 0; t < MQ_UNITS; ++t) {
+    w[t] = make_uint4(0, 0, 0, 0);
+    b[t] = 0;
+    const int r = at.first + t * at.step;
+    if (t < units && g_ok && r + 32 * i < count) {
+      w[t] = __ldcs(reinterpret_cast<const uint4*>(codes + (size_t)r * (p.K / 2)));
+      b[t] = __ldg(sc + r * 16);
+    }
+  }
+  // Two staging buffers: while one unit's rows leave, the next is made.
+  const uint32_t base = smem_u32(staging) + (uint32_t)(warp * (spread ? 1 : 2) * kUnit);
+#pragma unroll
+  for (int t = 0; t < MQ_UNITS; ++t) {
+    if (t >= units) break;
+    const int r = at.first + t * at.step;
+    const uint32_t buf = base + (t & 1) * kUnit;
+    if (t >= 2) {
+      if (lane < 4) bulk_wait_read<1>();
+      __syncwarp();
+    }
+    // 2^(b - 127): b = 0 is the subnormal 2^-127, 255 is NaN.
+    const float scale = __uint_as_float(b[t] == 255u ? 0x7FC00000u : b[t] == 0u ? 0x00400000u : b[t] << 23);
+    const float2 scale2 = make_float2(scale, scale);
+    const uint32_t out = buf + i * (kUnit / 4) + g * (32 * kSize);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      // Word c of the lane's codes, in an order that differs between the lanes
+      // that would meet in one bank.
+      const int c = (s + (g >> 1)) & 3;
+      const uint32_t lo = c & 1 ? w[t].y : w[t].x, hi = c & 1 ? w[t].w : w[t].z, word = c & 2 ? hi : lo;
+      float2 v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t h2;   // two E2M1 codes -> two fp16 values, exact
-        asm("{\n\t.reg .b8 lo, x1, x2, x3;\n\tmov.b32 {lo, x1, x2, x3}, %1;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %0, lo;\n\t}"
+        asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\tmov.b32 {x0, x1, x2, x3}, %1;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, x0;\n\t}"
             : "=r"(h2)
-            : "r"(w[i] >> (8 * j)));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-        v[2 * j] = __fmul_rn(f.x, scale);
-        v[2 * j + 1] = __fmul_rn(f.y, scale);
+            : "r"(word >> (8 * j)));
+        v[j] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h2)), scale2);
       }
-      const size_t at = (size_t)(row0 + r + 32 * i) * p.ldo + k;
       if constexpr (kDtype == kMxFp32) {
-        float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-        __stcs(out, make_float4(v[0], v[1], v[2], v[3]));
-        __stcs(out + 1, make_float4(v[4], v[5], v[6], v[7]));
+        sts128(out + 32 * c, make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                                        __float_as_uint(v[1].y)));
+        sts128(out + 32 * c + 16, make_uint4(__float_as_uint(v[2].x), __float_as_uint(v[2].y),
+                                             __float_as_uint(v[3].x), __float_as_uint(v[3].y)));
       } else {
-        __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at),
-               make_uint4(mx_pack16(v[0], v[1], false), mx_pack16(v[2], v[3], false), mx_pack16(v[4], v[5], false),
-                          mx_pack16(v[6], v[7], false)));
+        sts128(out + 16 * c, make_uint4(mx_pack16(v[0].x, v[0].y, false), mx_pack16(v[1].x, v[1].y, false),
+                                        mx_pack16(v[2].x, v[2].y, false), mx_pack16(v[3].x, v[3].y, false)));
       }
     }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane < 4) {
+      if (r + 32 * lane < count)
+        bulk_store(static_cast<uint8_t*>(p.out) + ((size_t)(row0 + r + 32 * lane) * p.ldo + k0) * kSize,
+                   buf + lane * (kUnit / 4), row_bytes);
+      bulk_commit();
+    }
   }
+  if (lane < 4) bulk_wait<0>();
 }
 
 // Scale blocks of the rows: those the groups' blocks can reach.
 long long row_blocks(int rows, int groups) { return groups == 0 ? ((long long)rows + 127) / 128 : rows / 128 + groups; }
 
-// With few tiles a warp takes one quad of rows, so that four times as many
-// warps share the latency; with many it takes four and loads ahead.
-constexpr long long MQ_FEW_TILES = 1024;
+// With few tiles a warp takes one unit, so that twice as many warps share the
+// latency (512 x 2048, 32 tiles: 2.15 us, against 2.34); with many it has all
+// of its units in flight (1024 x 4096, 128 tiles: 3.0 us, against 3.8).
+constexpr long long MQ_FEW_TILES = 128;
 
-template <class P, class Kernel>
-cudaError_t launch_rows(const P& p, Kernel kernel, cudaStream_t stream, bool pdl) {
+template <auto kKernel, int kWarps, int kUnit, int kBuffers, class P>
+cudaError_t launch_rows(const P& p, cudaStream_t stream, bool pdl) {
+  if (cudaError_t e = mx_allow_smem<kKernel>(kWarps * kBuffers * kUnit)) return e;
   const int k_slices = (p.K + MQ_COLS - 1) / MQ_COLS;
   const long long tiles = row_blocks(p.rows, p.groups) * k_slices;
-  const int parts = tiles < MQ_FEW_TILES ? 4 : 1;
+  const int spread = tiles < MQ_FEW_TILES;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * parts));
-  cfg.blockDim = dim3(MQ_THREADS);
+  cfg.gridDim = dim3((unsigned)(tiles * (32 / (kWarps * MQ_UNITS)) * (spread ? MQ_UNITS : 1)));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kWarps * (spread ? 1 : kBuffers) * kUnit;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   set_pdl(cfg, attr, pdl);
-  return cudaLaunchKernelEx(&cfg, kernel, p, k_slices, parts);
+  return cudaLaunchKernelEx(&cfg, kKernel, p, k_slices, spread);
+}
+
+template <int kDtype>
+cudaError_t launch_quantize(const MxQuantParams& p, cudaStream_t stream, bool pdl) {
+  constexpr int kWarps = quant_warps<kDtype>();
+  return launch_rows<mxfp4_quantize_kernel<kDtype>, kWarps, unit_bytes<kDtype>(), MQ_UNITS>(p, stream, pdl);
+}
+template <int kDtype>
+cudaError_t launch_dequantize(const MxDequantParams& p, cudaStream_t stream, bool pdl) {
+  return launch_rows<mxfp4_dequantize_kernel<kDtype>, 8, unit_bytes<kDtype>(), 2>(p, stream, pdl);
 }
 
 }  // namespace
 
 cudaError_t launch_mxfp4_quantize(const MxQuantParams& p, cudaStream_t stream, bool pdl) {
   switch (p.dtype) {
-    case kMxBf16: return launch_rows(p, mxfp4_quantize_kernel<kMxBf16>, stream, pdl);
-    case kMxFp16: return launch_rows(p, mxfp4_quantize_kernel<kMxFp16>, stream, pdl);
-    default: return launch_rows(p, mxfp4_quantize_kernel<kMxFp32>, stream, pdl);
+    case kMxBf16: return launch_quantize<kMxBf16>(p, stream, pdl);
+    case kMxFp16: return launch_quantize<kMxFp16>(p, stream, pdl);
+    default: return launch_quantize<kMxFp32>(p, stream, pdl);
   }
 }
 
 cudaError_t launch_mxfp4_dequantize(const MxDequantParams& p, cudaStream_t stream, bool pdl) {
-  if (p.dtype == kMxFp32) return launch_rows(p, mxfp4_dequantize_kernel<kMxFp32>, stream, pdl);
-  return launch_rows(p, mxfp4_dequantize_kernel<kMxBf16>, stream, pdl);
+  return p.dtype == kMxFp32 ? launch_dequantize<kMxFp32>(p, stream, pdl) : launch_dequantize<kMxBf16>(p, stream, pdl);
 }
 
 }  // namespace svdq

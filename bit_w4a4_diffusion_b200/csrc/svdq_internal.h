@@ -306,10 +306,11 @@ struct MxGemmTmaps {
 // 256 x 256 tiles on CTA pairs (SwiGLU: 256 rows x 128 hidden columns).
 cudaError_t launch_mxfp4_gemm_pair(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, cudaStream_t stream,
                                    bool pdl);
-// 128 weight rows x up to 128 (SwiGLU: 64) rows per CTA, the weight as the
-// M operand; t.act's box is kMxNarrowBox rows.
+// 128 weight rows x up to 64 rows per CTA, the weight as the M operand;
+// t.act's box is kMxNarrowBox rows.
 constexpr int kMxNarrowBox = 32;
-constexpr int kMxNarrowRows = 128, kMxNarrowRowsGlu = 64;
+constexpr int kMxNarrowRows = 64;
+constexpr int kMxNarrowPerSm = 2;   // CTAs per SM
 cudaError_t launch_mxfp4_gemm_narrow(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, int num_sms,
                                      cudaStream_t stream, bool pdl);
 

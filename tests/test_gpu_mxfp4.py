@@ -283,7 +283,7 @@ def steps_linear(x, w, bias=None, **kw):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N,K", [(8, 32), (136, 96), (1000, 544), (2056, 4096)])
 def test_linear_around_the_fused_limit(N, K, dtype):
-    """Up to 16 rows the product quantizes x itself: the same bits as the two
+    """Up to four rows the product quantizes x itself: the same bits as the two
     steps, below the limit and above, special values included."""
     rng = np.random.default_rng(N + K)
     w = B.to_device(B.mxfp4_pack_weights(F.bf16_bits(rng.standard_normal((N, K)).astype(np.float32))))
@@ -292,9 +292,36 @@ def test_linear_around_the_fused_limit(N, K, dtype):
     base[3, 8] = float("inf")
     base[5, 20:K] = 0
     base[6] *= 2.0 ** -18 if dtype == torch.float16 else 2.0 ** -120
-    for M in (1, 2, 7, 8, 9, 15, 16, 17, 40):
+    for M in (1, 2, 3, 4, 5, 8, 40):
         x = base[:M, 8:8 + K]
         same_bits(B.mxfp4_linear(x, w, bias=b), steps_linear(x, w, b))
+
+
+@pytest.mark.parametrize("M", [1, 4])
+def test_fused_layers_with_many_slices_and_tiles_per_cta(M):
+    """More weight tiles than CTAs and many K slices each: the ring goes round
+    often, at another stage for every tile."""
+    rng = np.random.default_rng(M)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    N, K = 128 * 300 + 8, 2848
+    x = C.rows(rng, M, K, torch.bfloat16).cuda()
+
+    def weight(E, n):
+        return {"codes": torch.randint(0, 256, (E, n, K // 2), dtype=torch.uint8, device="cuda", generator=g),
+                "scales": torch.randint(110, 118, (E, B.mxfp4_scale_bytes(n, K)), dtype=torch.uint8, device="cuda",
+                                        generator=g), "N": n, "K": K, "E": E}
+    w = weight(1, N)
+    want = steps_linear(x, w)
+    for _ in range(5):
+        same_bits(B.mxfp4_linear(x, w), want)
+    up, off = weight(2 * 4, 128 * 100), cuda([0, 1, 1, M, M], torch.int32)
+    down = {"codes": torch.randint(0, 256, (4, K, 6400), dtype=torch.uint8, device="cuda", generator=g),
+            "scales": torch.randint(110, 118, (4, B.mxfp4_scale_bytes(K, 12800)), dtype=torch.uint8, device="cuda",
+                                    generator=g), "N": K, "K": 12800, "E": 4}
+    q = B.mxfp4_quantize(x, offsets=off)
+    want = B.mxfp4_grouped_gemm(*B.mxfp4_grouped_gemm_swiglu_quant(*q, off, up), off, down)
+    for _ in range(5):
+        same_bits(B.mxfp4_grouped_mlp_swiglu(x, off, up, down), want)
 
 
 # ----------------------------------------------------------------- grouped --
@@ -362,13 +389,13 @@ def test_grouped_linear_gathers(monkeypatch, kernel):
     assert (y[230:] == 2.0).all()
 
 
-SMALL = {   # offsets, rows: up to 64 rows the grouped layers quantize x themselves
+SMALL = {   # offsets, rows: up to 16 rows the grouped layers quantize x themselves
     "one row": ([0, 1], 1),
-    "one group": ([0, 64], 64),
-    "all in the last": ([0, 0, 0, 0, 63], 64),
-    "a few each": ([0, 3, 3, 20, 37, 64], 64),
-    "rows of no group": ([5, 6, 40, 41], 50),
-    "above the limit": ([0, 30, 65], 65),
+    "one group": ([0, 16], 16),
+    "all in the last": ([0, 0, 0, 0, 15], 16),
+    "a few each": ([0, 3, 3, 5, 6, 15], 15),
+    "rows of no group": ([2, 3, 12, 13], 16),
+    "above the limit": ([0, 8, 17], 17),
 }
 
 

@@ -123,7 +123,7 @@ def test_sizes():
     assert B.mxfp4_scale_bytes(1, 48) == -1 and B.mxfp4_scale_bytes(-1, 32) == -1
     assert B.mxfp4_scale_bytes(1, 32, groups=513) == -1
     assert B.mxfp4_workspace_bytes(17, 32) == 512 + 512
-    assert B.mxfp4_workspace_bytes(16, 32) == 0 and B.mxfp4_workspace_bytes(64, 32, groups=3) == 0
+    assert B.mxfp4_workspace_bytes(4, 32) == 0 and B.mxfp4_workspace_bytes(16, 32, groups=3) == 0
     assert B.mxfp4_mlp_workspace_bytes(4, 100, 64, 96) == (B.mxfp4_workspace_bytes(100, 64, 4) +
                                                            B.mxfp4_workspace_bytes(100, 96, 4))
     assert B.mxfp4_mlp_workspace_bytes(4, 8, 64, 96) == 512 + (4 * 512)
@@ -131,7 +131,7 @@ def test_sizes():
 
 
 def test_sizes_agree_with_the_library():
-    for rows in (0, 1, 127, 128, 129, 1000):
+    for rows in (0, 1, 4, 5, 16, 17, 127, 128, 129, 1000):
         for K in (32, 96, 128, 4128):
             assert B.mxfp4_scale_bytes(rows, K) == B.lib.mxfp4_scale_bytes(rows, K)
             for groups in (0, 1, 7, 512, 513, -1):
