@@ -541,21 +541,24 @@ def _mx_empty(shape, dtype, device):
 
 
 def _mx_rows(t, name, dtypes):
-    """(mxfp4 dtype, row stride) of a CUDA matrix whose rows are contiguous."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2):
+    """(mxfp4 dtype, rows, columns, row stride) of a CUDA matrix whose rows
+    are contiguous; ``dtypes`` maps the accepted torch types."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or not t.is_cuda or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return MXFP4_DTYPES[t.dtype], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return dtypes[t.dtype], rows, cols, ld if rows > 1 else cols
 
 
 def _mx_like(t, name, device, dtype, count):
     """Data pointer of a contiguous tensor of ``count`` elements, or of None."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device:
         raise TypeError(f"{name} must be a {dtype} tensor on {device}")
-    if not t.is_contiguous() or t.numel() != count:
+    if t.numel() != count or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous and have {count} elements (it has {t.numel()})")
     return t.data_ptr()
 
@@ -567,6 +570,16 @@ def _mx_weight(w, name, device, N, K, matrices):
             _mx_like(w["scales"], name + " scales", device, torch.uint8, matrices * mxfp4_scale_bytes(N, K)))
 
 
+def _mx_index(row_index, x_rows, device):
+    """(rows, address) of a row index, or of none: row i is row i of x."""
+    if row_index is None:
+        return x_rows, None
+    if not isinstance(row_index, torch.Tensor):
+        raise TypeError("row_index must be an int32 tensor")
+    rows = row_index.numel()
+    return rows, _mx_like(row_index, "row_index", device, torch.int32, rows)
+
+
 def _mx_groups(offsets, device):
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
         raise TypeError("offsets must be an int32 tensor [groups + 1]")
@@ -576,10 +589,22 @@ def _mx_groups(offsets, device):
 def _mx_out(y, rows, N, dtype, device):
     if y is None:
         return _mx_empty((rows, N), dtype, device), N
-    _, ldy = _mx_rows(y, "y", (dtype,))
-    if y.shape != (rows, N) or y.device != device:
+    _, y_rows, y_cols, ldy = _mx_rows(y, "y", {dtype: 0})
+    if y_rows != rows or y_cols != N or y.device != device:
         raise ValueError(f"y must be [{rows}, {N}] on {device}")
     return y, ldy
+
+
+def _mx_quantized(out, rows, K, size, device):
+    """Codes [rows, K/2] and scales (``size`` bytes): the caller's pair,
+    checked, or new; and their addresses."""
+    if out is None:
+        codes = _mx_empty((rows, K // 2), torch.uint8, device)
+        scales = torch.empty(size, dtype=torch.uint8, device=device)
+        return codes, scales, codes.data_ptr(), scales.data_ptr()
+    codes, scales = out
+    return (codes, scales, _mx_like(codes, "codes", device, torch.uint8, rows * (K // 2)),
+            _mx_like(scales, "scales", device, torch.uint8, size))
 
 
 def _mx_workspace(workspace, need, device):
@@ -596,11 +621,11 @@ def _mx_workspace(workspace, need, device):
 
 
 def _mx_status(dev_status, device):
-    return _mx_like(dev_status, "dev_status", device, torch.int32, 1)
+    return None if dev_status is None else _mx_like(dev_status, "dev_status", device, torch.int32, 1)
 
 
-_MX_INPUT = (torch.bfloat16, torch.float16, torch.float32)
-_MX_LAYER = (torch.bfloat16, torch.float16)
+_MX_INPUT = MXFP4_DTYPES
+_MX_LAYER = {torch.bfloat16: 0, torch.float16: 1}
 
 
 def mxfp4_quantize(x, offsets=None, row_index=None, out=None, dev_status=None, stream=None):
@@ -608,21 +633,16 @@ def mxfp4_quantize(x, offsets=None, row_index=None, out=None, dev_status=None, s
     tiled E8M0 scales uint8).  ``row_index`` (int32 [rows]): row i is
     x[row_index[i]].  ``offsets`` (int32 [groups + 1]): scales in the grouped
     layout; rows of no group are skipped."""
-    dtype, ldx = _mx_rows(x, "x", _MX_INPUT)
+    dtype, x_rows, K, ldx = _mx_rows(x, "x", _MX_INPUT)
     dev = x.device
-    x_rows, K = x.shape
-    rows = x_rows if row_index is None else row_index.numel()
+    rows, idx = _mx_index(row_index, x_rows, dev)
     groups, off = (0, None) if offsets is None else _mx_groups(offsets, dev)
     size = mxfp4_scale_bytes(rows, K, groups)
     if size < 0:
         raise SvdqError(2, f"unsupported shape rows={rows} K={K} groups={groups}")
-    if out is None:
-        out = (_mx_empty((rows, K // 2), torch.uint8, dev), torch.empty(size, dtype=torch.uint8, device=dev))
-    codes, scales = out
-    _mx_call(dev, stream, lib.mxfp4_quantize, dtype, rows, K, x.data_ptr(), ldx,
-             _mx_like(row_index, "row_index", dev, torch.int32, rows), x_rows, groups, off,
-             _mx_like(codes, "codes", dev, torch.uint8, rows * (K // 2)),
-             _mx_like(scales, "scales", dev, torch.uint8, size), _mx_status(dev_status, dev))
+    codes, scales, codes_ptr, scales_ptr = _mx_quantized(out, rows, K, size, dev)
+    _mx_call(dev, stream, lib.mxfp4_quantize, dtype, rows, K, x.data_ptr(), ldx, idx, x_rows, groups, off, codes_ptr,
+             scales_ptr, _mx_status(dev_status, dev))
     return codes, scales
 
 
@@ -685,9 +705,8 @@ def _mx_gemm(codes, scales, offsets, w, bias, dtype, y, dev_status, stream):
 
 def mxfp4_linear(x, w, bias=None, y=None, workspace=None, dev_status=None, stream=None):
     """y = Q(x) deq(W)^T + bias for x bf16 or fp16 [M, K]; y has x's type."""
-    dtype, ldx = _mx_rows(x, "x", _MX_LAYER)
+    dtype, M, K, ldx = _mx_rows(x, "x", _MX_LAYER)
     dev = x.device
-    M, K = x.shape
     N = w["N"]
     wc, ws = _mx_weight(w, "w", dev, N, K, 1)
     y, ldy = _mx_out(y, M, N, x.dtype, dev)
@@ -702,17 +721,16 @@ def mxfp4_grouped_linear(x, offsets, w, row_index=None, bias=None, y=None, works
                          stream=None):
     """mxfp4_linear per row group: row i of y [rows, N] is row i of x, or
     x[row_index[i]], times the weight of the group that owns row i."""
-    dtype, ldx = _mx_rows(x, "x", _MX_LAYER)
+    dtype, x_rows, K, ldx = _mx_rows(x, "x", _MX_LAYER)
     dev = x.device
-    x_rows, K = x.shape
-    rows = x_rows if row_index is None else row_index.numel()
+    rows, idx = _mx_index(row_index, x_rows, dev)
     N = w["N"]
     groups, off = _mx_groups(offsets, dev)
     wc, ws = _mx_weight(w, "w", dev, N, K, groups)
     y, ldy = _mx_out(y, rows, N, x.dtype, dev)
     workspace, ws_ptr, ws_size = _mx_workspace(workspace, mxfp4_workspace_bytes(rows, K, groups), dev)
     _mx_call(dev, stream, lib.mxfp4_grouped_linear, dtype, groups, rows, N, K, x.data_ptr(), ldx,
-             _mx_like(row_index, "row_index", dev, torch.int32, rows), x_rows, off, wc, ws,
+             idx, x_rows, off, wc, ws,
              _mx_like(bias, "bias", dev, x.dtype, groups * N), y.data_ptr(), ldy, ws_ptr, ws_size, _mx_status(dev_status, dev))
     return y
 
@@ -735,15 +753,11 @@ def mxfp4_grouped_gemm_swiglu_quant(codes, scales, offsets, w, bias=None, dtype=
     size = mxfp4_scale_bytes(rows, width, groups)
     if size < 0:
         raise SvdqError(2, f"unsupported shape rows={rows} I={width} groups={groups}")
-    if out is None:
-        out = (_mx_empty((rows, width // 2), torch.uint8, dev), torch.empty(size, dtype=torch.uint8, device=dev))
-    h_codes, h_scales = out
+    h_codes, h_scales, hc, hs = _mx_quantized(out, rows, width, size, dev)
     _mx_call(dev, stream, lib.mxfp4_grouped_gemm_swiglu_quant, MXFP4_DTYPES[dtype], groups, rows, width, K, off,
              _mx_like(codes, "codes", dev, torch.uint8, rows * (K // 2)),
              _mx_like(scales, "scales", dev, torch.uint8, mxfp4_scale_bytes(rows, K, groups)), wc, ws,
-             _mx_like(bias, "bias", dev, dtype, 2 * groups * width),
-             _mx_like(h_codes, "out codes", dev, torch.uint8, rows * (width // 2)),
-             _mx_like(h_scales, "out scales", dev, torch.uint8, size), _mx_status(dev_status, dev))
+             _mx_like(bias, "bias", dev, dtype, 2 * groups * width), hc, hs, _mx_status(dev_status, dev))
     return h_codes, h_scales
 
 
@@ -752,10 +766,9 @@ def mxfp4_grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index=None, up_bias=N
     """The experts' MLP y = down(SwiGLU(up(x))) per row group: w_up two
     matrices [I, K] per group (gate, other), w_down [groups, K, I]; the hidden
     rows are quantized in the up product's epilogue."""
-    dtype, ldx = _mx_rows(x, "x", _MX_LAYER)
+    dtype, x_rows, K, ldx = _mx_rows(x, "x", _MX_LAYER)
     dev = x.device
-    x_rows, K = x.shape
-    rows = x_rows if row_index is None else row_index.numel()
+    rows, idx = _mx_index(row_index, x_rows, dev)
     width = w_up["N"]
     groups, off = _mx_groups(offsets, dev)
     uc, us = _mx_weight(w_up, "w_up", dev, width, K, 2 * groups)
@@ -763,7 +776,7 @@ def mxfp4_grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index=None, up_bias=N
     y, ldy = _mx_out(y, rows, K, x.dtype, dev)
     workspace, ws_ptr, ws_size = _mx_workspace(workspace, mxfp4_mlp_workspace_bytes(groups, rows, K, width), dev)
     _mx_call(dev, stream, lib.mxfp4_grouped_mlp_swiglu, dtype, groups, rows, K, width, x.data_ptr(), ldx,
-             _mx_like(row_index, "row_index", dev, torch.int32, rows), x_rows, off, uc, us,
+             idx, x_rows, off, uc, us,
              _mx_like(up_bias, "up_bias", dev, x.dtype, 2 * groups * width), dc, ds,
              _mx_like(down_bias, "down_bias", dev, x.dtype, groups * K), y.data_ptr(), ldy, ws_ptr, ws_size, _mx_status(dev_status, dev))
     return y

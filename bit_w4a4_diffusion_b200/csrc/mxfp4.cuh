@@ -162,8 +162,9 @@ struct MxSched {
   int pre[kMxMaxGroups + 1];
 };
 
-// Filled by one whole warp.  Offsets that decrease or leave [0, rows] give an
-// empty schedule and a status code.
+// Filled by one whole warp; all loads go out before the first is used.
+// Offsets that decrease or leave [0, rows] give an empty schedule and a status
+// code.
 SVDQ_DEV void mx_build_sched(MxSched* s, int groups, const int* offsets, int rows, int tile_rows, int* dev_status) {
   const int lane = threadIdx.x & 31;
   if (groups == 0) {
@@ -175,26 +176,36 @@ SVDQ_DEV void mx_build_sched(MxSched* s, int groups, const int* offsets, int row
     }
     return;
   }
+  constexpr int kRounds = kMxMaxGroups / 32 + 1;   // groups + 1 offsets, 32 at a time
+  int off[kRounds];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int e = 32 * i + lane;
+    off[i] = e <= groups ? __ldg(offsets + e) : 0;
+  }
   int run = 0;
   bool bad = false;
-  for (int base = 0; base < groups; base += 32) {
-    const int e = base + lane;
-    int lo = 0, hi = 0;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    if (32 * i > groups) break;
+    const int e = 32 * i + lane, lo = off[i];
+    int hi = __shfl_down_sync(0xffffffffu, lo, 1);
+    const int next = i + 1 < kRounds ? __shfl_sync(0xffffffffu, off[i + 1 < kRounds ? i + 1 : i], 0) : 0;
+    if (lane == 31) hi = next;
+    int t = 0;
     if (e < groups) {
-      lo = offsets[e];
-      hi = offsets[e + 1];
+      const bool wrong = lo < 0 || hi < lo || hi > rows;
+      bad |= wrong;
+      t = wrong ? 0 : (hi - lo + tile_rows - 1) / tile_rows;
     }
-    bad |= lo < 0 || hi < lo || hi > rows;
-    int t = bad ? 0 : (hi - lo + tile_rows - 1) / tile_rows;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, t, d);
       if (lane >= d) t += o;
     }
-    if (e < groups) {
+    if (e <= groups) {
       s->off[e] = lo;
-      s->pre[e + 1] = run + t;
-      if (e == groups - 1) s->off[groups] = hi;
+      if (e < groups) s->pre[e + 1] = run + t;
     }
     run += __shfl_sync(0xffffffffu, t, 31);
   }
@@ -207,13 +218,24 @@ SVDQ_DEV void mx_build_sched(MxSched* s, int groups, const int* offsets, int row
 }
 
 // One tile: row tile `mt` of group e (rows row0 .. row0 + rows - 1 of the
-// matrix, scale block `block`), column tile nt.  `tile` only grows between
-// calls of one walker, so the group pointer moves forward.
+// matrix), column tile nt.  `tile` (less than the tile count) only grows
+// between calls of one walker, which keeps the group it is in.
 struct MxTile {
   int e, mt, nt, row0, rows;
 };
-SVDQ_DEV MxTile mx_decode_tile(const MxSched* s, int tile, int tiles_n, int tile_rows, int& e) {
-  while (tile >= s->pre[e + 1] * tiles_n) ++e;
+SVDQ_DEV MxTile mx_decode_tile(const MxSched* s, int groups, int tile, int tiles_n, int tile_rows, int& e) {
+  if (tile >= s->pre[e + 1] * tiles_n) {
+    // The first group whose tiles end behind this one.
+    int lo = e + 1, hi = groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (tile >= s->pre[mid + 1] * tiles_n)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    e = lo;
+  }
   const int first = s->pre[e];
   const int local = tile - first * tiles_n, mts = s->pre[e + 1] - first;
   MxTile t;

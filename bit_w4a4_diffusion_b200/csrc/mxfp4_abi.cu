@@ -16,6 +16,8 @@ using namespace svdq;
 
 namespace {
 
+static_assert(MXFP4_FUSED_ROWS <= kMxFusedRows && MXFP4_FUSED_GROUPED_ROWS <= kMxFusedRows, "fused kernels' limit");
+static_assert(MXFP4_MAX_GROUPS == kMxMaxGroups, "header and kernels agree");
 constexpr int kMaxRows = 1 << 30;   // keeps row + tile arithmetic inside 32 bits
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -149,12 +151,19 @@ bool use_pair(int groups, int rows, int N, bool swiglu, int sms) {
   return rows / (groups == 0 ? 1 : groups) > (swiglu ? 128 : 96);
 }
 
-// CTAs that share one tile's K: as many as fit the chip once, at most one per
-// 256-column slice of K.
-int choose_splits(long long tiles, int K, int sms) {
-  const int slices = (K + 255) / 256;
+// CTAs (a cluster) that share one tile's K: as many as there are SMs for, each
+// with at least four 256-column slices (SwiGLU, whose ring holds two: two).
+// GPU time, us, of 1, 2, 4, 8 CTAs:
+//   1 row, 4096 x 4096 (32 tiles): 8.7, 6.8, 5.9, 6.2;  64 rows: 9.8, 9.1, 7.9, 9.7
+//   77 rows, 5000 x 2080 (80 tiles): 8.0, 9.6
+//   2 experts' rows, 4096 x 4096 (64 tiles): 10.0, 8.6, 8.2, 13.0;  SwiGLU: 16.2, 12.9, 11.8, 17.2
+// Up to two CTAs per SM would take the last 5% of a single product with few
+// rows, but in the MLP they leave the next product no room to load its
+// weights ahead (8 experts, 2048 x 1024: 17.1 us against 15.8).
+int choose_splits(long long tiles, int K, bool swiglu, int sms) {
+  const int slices = (K + 255) / 256, least = swiglu ? 2 : 4;
   for (int s = 8; s > 1; s /= 2)
-    if (tiles * s <= sms && slices >= s) return s;
+    if (tiles * s <= sms && slices >= s * least) return s;
   return 1;
 }
 
@@ -220,7 +229,7 @@ int product(const Device& d, const Product& g, cudaStream_t stream) {
   p.timeout_ns = svdq_get_timeout_ns();
   if (pair) return cuda_status(launch_mxfp4_gemm_pair(p, t, g.swiglu, stream, d.pdl), "mxfp4_gemm_pair launch");
   const long long m_tiles = narrow_m_tiles(g.groups, g.rows);
-  p.splits = choose_splits(m_tiles * ((g.N + 127) / 128), g.K, d.sms);
+  p.splits = choose_splits(m_tiles * ((g.N + 127) / 128), g.K, g.swiglu, d.sms);
   return cuda_status(launch_mxfp4_gemm_narrow(p, t, g.swiglu, d.sms, stream, d.pdl), "mxfp4_gemm_narrow launch");
 }
 

@@ -76,6 +76,7 @@ struct Cfg {
   static_assert(kTmemSf + kStages * kSfCols <= TMEM_COLS, "accumulators and scale buffers fit tensor memory");
 };
 
+static_assert(kMxFusedRows <= 32, "a warp's lanes hold the row index");
 template <bool kGlu, int kX>
 constexpr int num_threads() { return (QUANT_WARP + (kX == kNoX ? 0 : Cfg<kGlu>::kStages)) * 32; }   // a quantizer warp per stage
 
@@ -152,6 +153,8 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
   // Offsets are an input like the weights: with weights_early both were
   // complete before the preceding kernel began.
   if (!p.weights_early) pdl_wait();
+  int row_index = 0;
+  if (kFused && warp >= QUANT_WARP && p.row_index != nullptr && lane < p.rows) row_index = __ldg(p.row_index + lane);
   if (warp == 0) mx_build_sched(&ctl->sched, p.groups, p.offsets, p.rows, ROWS, p.dev_status);
   __syncwarp();
   tc_fence_before();
@@ -161,9 +164,10 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
   pdl_launch_dependents();
 
   const MxSched* const sched = &ctl->sched;
+  const int groups = p.groups == 0 ? 1 : p.groups;
   const int k_slices = (p.K + 255) / 256, k_chunks = (p.K + 127) / 128;
   const int tiles_n = (p.N + BW - 1) / BW;
-  const int num_tiles = sched->pre[p.groups == 0 ? 1 : p.groups] * tiles_n;
+  const int num_tiles = sched->pre[groups] * tiles_n;
   const int splits = p.splits;
   const uint32_t rank = splits > 1 ? cluster_ctarank() : 0;
   // This CTA's part of K (whole K without splits) and its tiles.
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
                        pol_a);
     };
     for (int tile = t_first; tile < num_tiles && ok; tile += t_step) {
-      const MxTile t = mx_decode_tile(sched, tile, tiles_n, ROWS, e);
+      const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
       const int boxes = (t.rows + kMxNarrowBox - 1) / kMxNarrowBox;
       int kb = kb_begin;
       if (!act_ready) {
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     uint32_t phase = 0;
     bool ok = true;
     for (int tile = t_first; tile < num_tiles && ok; tile += t_step, ++seq) {
-      const MxTile t = mx_decode_tile(sched, tile, tiles_n, ROWS, e);
+      const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
       const int a = seq % C::kBufs;
       if (!mbar_wait_warp(smem_u32(&ctl->acc_empty[a]), ((seq / C::kBufs) & 1) ^ 1, wctx, kDevTimeoutMma)) break;
       tc_fence_after();
@@ -353,10 +357,12 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
         }
       };
       using Raw = typename E::Raw;
+      // The whole row index (at most 32 rows), loaded at the kernel's start.
+      const int index = row_index;
       int count = 0, e = 0;    // slices of all tiles so far
       bool ok = true;
       for (int tile = t_first; tile < num_tiles && ok; tile += t_step) {
-        const MxTile t = mx_decode_tile(sched, tile, tiles_n, ROWS, e);
+        const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
         for (int kb = kb_begin; kb < kb_end && ok; ++kb, ++count) {
           if (count % C::kStages != stage) continue;
           const uint32_t phase = (uint32_t)(count / C::kStages) & 1;
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
               if (i < n) {
                 int src = t.row0 + r0 + i;
                 if (p.row_index != nullptr) {
-                  src = __ldg(p.row_index + src);
+                  src = __shfl_sync(0xffffffffu, index, src);
                   if (src < 0 || src >= p.x_rows) lost |= 1u << i;
                 }
                 if (k < p.K && !((lost >> i) & 1u)) raw[i] = E::load_now(x + (size_t)src * p.ldx * E::kSize);
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     const bool fp16 = p.fp16 != 0;
     int e = 0, seq = 0, out_seq = 0;
     for (int tile = t_first; tile < num_tiles; tile += t_step, ++seq) {
-      const MxTile t = mx_decode_tile(sched, tile, tiles_n, ROWS, e);
+      const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
       const int a = seq % C::kBufs;
       const int n0 = t.nt * BW, n = n0 + 32 * q + lane;
       float b0 = 0.f, b1 = 0.f;
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     cluster_sync();
     if (t_first < num_tiles) {
       int e = 0;
-      const MxTile t = mx_decode_tile(sched, t_first, tiles_n, ROWS, e);
+      const MxTile t = mx_decode_tile(sched, groups, t_first, tiles_n, ROWS, e);
       const bool fp16 = p.fp16 != 0;
       const int n = t.nt * BW + 4 * lane;
       const bool in_n = n < p.N;          // N is a multiple of 8 (SwiGLU: 32)

@@ -118,11 +118,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem = ctl->tmem_base;
 
   const MxSched* const sched = &ctl->sched;
+  const int groups = p.groups == 0 ? 1 : p.groups;
   const int k_slices = (p.K + 255) / 256, k_chunks = (p.K + 127) / 128;
   constexpr int kTileCols = kGlu ? BN_HALF : BN;             // output columns per tile
   const int tiles_n = (p.N + kTileCols - 1) / kTileCols;
   const int blocks_n = (p.N + 127) / 128;                    // 128-row scale blocks of one weight matrix
-  const int num_tiles = sched->pre[p.groups == 0 ? 1 : p.groups] * tiles_n;
+  const int num_tiles = sched->pre[groups] * tiles_n;
   const WaitCtx wctx{&ctl->abort_flag, p.dev_status, p.timeout_ns};
 
   if (warp == PRODUCER_WARP) {
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     const uint64_t pol = policy_evict_last();   // other tiles read every operand again
     for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
-      const MxTile t = mx_decode_tile(sched, tile, tiles_n, 2 * BM, e);
+      const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, 2 * BM, e);
       const int row0 = t.row0 + (int)rank * BM;
       const int block_a = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + 2 * t.mt + (int)rank;
       // Weight rows and scale blocks: SwiGLU's tile takes the same 128 rows of
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t acc_phase = 0;
     int store_seq = 0, e = 0;
     for (int tile = pair; tile < num_tiles; tile += num_pairs) {
-      const MxTile t = mx_decode_tile(sched, tile, tiles_n, 2 * BM, e);
+      const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, 2 * BM, e);
       const int slab = (int)rank * BM + 32 * q;        // the warp's first row within the tile
       const int valid = min(32, t.rows - slab);        // its rows inside the group (may be <= 0)
       const int row0 = t.row0 + slab;

@@ -311,6 +311,7 @@ cudaError_t launch_mxfp4_gemm_pair(const MxGemmParams& p, const MxGemmTmaps& t, 
 constexpr int kMxNarrowBox = 32;
 constexpr int kMxNarrowRows = 64;
 constexpr int kMxNarrowPerSm = 2;   // CTAs per SM
+constexpr int kMxFusedRows = 16;    // most rows of a product that quantizes x itself
 cudaError_t launch_mxfp4_gemm_narrow(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, int num_sms,
                                      cudaStream_t stream, bool pdl);
 
