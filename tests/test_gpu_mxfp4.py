@@ -687,6 +687,24 @@ def test_stream_argument():
     same_bits(y, want)
 
 
+def test_stream_argument_owns_what_the_call_allocates():
+    """Output and workspace of a call on another stream come from that
+    stream's memory: work queued on the current stream does not get them."""
+    x, off, up, down = layer_set(5, T=200)
+    want = B.mxfp4_grouped_mlp_swiglu(x, off, up, down)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for handle in (st, st.cuda_stream):
+        got = []
+        for _ in range(20):
+            got.append(B.mxfp4_grouped_mlp_swiglu(x, off, up, down, stream=handle))
+            junk = torch.full((1 << 20,), 0xAB, dtype=torch.uint8, device="cuda")
+            del junk
+        torch.cuda.synchronize()
+        for y in got:
+            same_bits(y, want)
+
+
 def test_runs_are_bit_identical():
     """No atomics and a fixed order: the same call gives the same bits, also
     where a cluster splits K."""
