@@ -24,7 +24,8 @@ CXX_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-pthread", "-I"
              "-I", "/usr/local/cuda/include"]
 
 CU_SOURCES = ["abi.cu", "quantize_act.cu", "quantize_nvfp4.cu", "gemm_nvfp4.cu", "gemm_nvfp4_pair.cu", "gemm_int4.cu", "gemm_int4_pair.cu", "dequant_int4.cu", "awq_gemm.cu", "noalloc.cu",
-              "mxfp4_abi.cu", "mxfp4_quant.cu", "mxfp4_gemm_pair.cu", "mxfp4_gemm_narrow.cu"]
+              "mxfp4_abi.cu", "mxfp4_quant.cu", "mxfp4_gemm_pair.cu",
+              "mxfp4_gemm_pair_swiglu.cu", "mxfp4_gemm_narrow.cu"]
 CXX_SOURCES = ["pack.cpp", "calib.cpp", "mxfp4_pack.cpp"]
 
 

@@ -247,6 +247,17 @@ SVDQ_DEV MxTile mx_decode_tile(const MxSched* s, int groups, int tile, int tiles
   return t;
 }
 
+// The same with a group's rows dealt out evenly, in multiples of 128, over as
+// many tiles as tile_rows makes of them.
+SVDQ_DEV MxTile mx_decode_tile_even(const MxSched* s, int groups, int tile, int tiles_n, int tile_rows, int& e) {
+  MxTile t = mx_decode_tile(s, groups, tile, tiles_n, tile_rows, e);
+  const int first = s->off[e], count = s->off[e + 1] - first, mts = s->pre[e + 1] - s->pre[e];
+  const int each = ((count + mts - 1) / mts + 127) & ~127;
+  t.row0 = first + t.mt * each;
+  t.rows = min(count - t.mt * each, each);
+  return t;
+}
+
 // ------------------------------------------------------------------ products
 // Instruction descriptor of a block-scaled product of E2M1 operands with E8M0
 // scales; `step` (0 or 1) picks which two of the four scale bytes of a 32-bit

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -167,6 +168,21 @@ int choose_splits(long long tiles, int K, bool swiglu, int sms) {
   return 1;
 }
 
+// Parts of the pair kernel's tile: 1 (256 columns) or 2 (384), whichever takes
+// fewer cycles over the rounds of the chip's CTA pairs.  A slice takes 615 or
+// 809 cycles, a tile's end 1400 or 2100.  1 / 2, us: 8192^3 186.9 / 184.3;
+// 4096 x 12288 x 4096 79.3 / 74.1; 16 groups of 1024, 4096 x 2048 73.1 / 70.4.
+int choose_parts(int groups, int rows, int N, int K, int sms) {
+  const double slices = (K + 255) / 256, pairs = sms / 2;
+  auto cycles = [&](int cols, double slice, double end) {
+    // Groups end anywhere: half a tile more for each.
+    const double tiles = (groups == 0 ? (rows + 255) / 256 : rows / 256.0 + groups * 0.5) * ((N + cols - 1) / cols);
+    const double rounds = groups == 0 ? std::ceil(tiles / pairs) : std::max(1.0, tiles / pairs);
+    return rounds * (slices * slice + end);
+  };
+  return cycles(kMxPairCols<1>, 615, 1400) <= cycles(kMxPairCols<2>, 809, 2100) ? 1 : 2;
+}
+
 struct Product {
   int dtype, rows, N, K, groups;
   const int* offsets;
@@ -186,11 +202,12 @@ int product(const Device& d, const Product& g, cudaStream_t stream) {
   const int groups = g.groups == 0 ? 1 : g.groups;
   const long long matrices = (long long)groups * (g.swiglu ? 2 : 1);
   const bool pair = g.x == nullptr && use_pair(g.groups, g.rows, g.N, g.swiglu, d.sms);
+  const int parts = pair && !g.swiglu ? choose_parts(g.groups, g.rows, g.N, g.K, d.sms) : 0;
   MxGemmTmaps t;
   const uint64_t sfa_rows = (uint64_t)scale_blocks(g.groups, g.rows) * k_chunks * 2;
   const uint64_t sfw_rows = (uint64_t)matrices * ((g.N + 127) / 128) * k_chunks * 2;
   bool ok = encode_tmap_2d(&t.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, g.K / 2, (uint64_t)matrices * g.N, g.K / 2,
-                           128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+                           128, parts == 2 ? kMxPairCols<2> / 4 : 128, CU_TENSOR_MAP_SWIZZLE_128B);
   if (g.x == nullptr) {
     ok = ok && encode_tmap_2d(&t.act, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.act_codes, g.K / 2, g.rows, g.K / 2, 128,
                               pair ? 128 : kMxNarrowBox, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -227,7 +244,9 @@ int product(const Device& d, const Product& g, cudaStream_t stream) {
   p.splits = 1;
   p.dev_status = d.status;
   p.timeout_ns = svdq_get_timeout_ns();
-  if (pair) return cuda_status(launch_mxfp4_gemm_pair(p, t, g.swiglu, stream, d.pdl), "mxfp4_gemm_pair launch");
+  if (pair && g.swiglu)
+    return cuda_status(launch_mxfp4_gemm_pair_swiglu(p, t, stream, d.pdl), "mxfp4_gemm_pair_swiglu launch");
+  if (pair) return cuda_status(launch_mxfp4_gemm_pair(p, t, parts, stream, d.pdl), "mxfp4_gemm_pair launch");
   const long long m_tiles = narrow_m_tiles(g.groups, g.rows);
   p.splits = choose_splits(m_tiles * ((g.N + 127) / 128), g.K, g.swiglu, d.sms);
   return cuda_status(launch_mxfp4_gemm_narrow(p, t, g.swiglu, d.sms, stream, d.pdl), "mxfp4_gemm_narrow launch");

@@ -1,26 +1,32 @@
 // MXFP4 products with many rows per group, on CTA pairs (tcgen05
-// .cta_group::2): 256 rows x 256 weight rows per tile.
+// .cta_group::2): 256 rows x 256 or 384 weight rows per tile.
 //
 //   D[m, n] = sum_b Xa[m, b] Xw[n, b] sum_{k in b} a[m, k] w[n, k]    (kind::mxf4)
 //   y = round16(D + bias)
-//   SwiGLU: the tile's 256 weight rows are 128 gate rows and 128 other rows;
-//   h = g sigmoid(g) u, quantized to MXFP4 for the next product
 //
-// What bounds it: the tensor pipe, as far as operands arrive; a 256-column K
-// slice of a tile is 35 KB per SM (rows 16 KB, half of the weight rows 16 KB,
-// their scales 3 KB) for 256 x 256 x 256 multiply-adds on two SMs.
+// What bounds it: power, and the tensor pipe.  A 256-column K slice takes 615
+// cycles with one part of 256 weight rows and 809 with two of 192 (512 and 768
+// at the rate of the data sheet; the rest is the scale copies), and a tile
+// another 1400 or 2100 while its accumulator is emptied, for which tensor
+// memory has no second one.  At 8192^3 that is 295 or 280 thousand cycles, but
+// the GPU then runs at about 1.5 GHz instead of 1.965: 187 and 184 us, 5.9 and
+// 6.0 PFLOP/s, where cuBLAS's NVFP4 product reaches 6.1.
 //
 // A cluster of two CTAs computes a tile: CTA r holds rows [128 r, + 128) of
-// the tile's rows and of its weight rows (SwiGLU: CTA 0 the gate's, CTA 1 the
-// other factor's), the tensor cores exchange the weight halves, and each CTA
-// accumulates its 128 rows x 256 columns in its own tensor memory: columns
-// 0-255, and above them one 24-column scale buffer per pipeline stage, filled
-// by the MMA warp itself (tcgen05.cp) right before the MMAs that read it and
-// reused with the stage, so neither needs a barrier of its own.
+// the tile's rows and half of each part's weight rows, the tensor cores
+// exchange the weight halves, and each CTA accumulates its 128 rows x all
+// columns in its own tensor memory, and above them one scale buffer per
+// pipeline stage, filled by the MMA warp itself (tcgen05.cp) right before the
+// MMAs that read it and reused with the stage, so neither needs a barrier of
+// its own.
 //
 // Row groups may end anywhere.  A 32-row slab that lies inside its group is
 // stored by TMA; the group's last, short slab by predicated 16-byte stores,
 // so that rows of the next group and rows behind the last one stay untouched.
+// (With the weight as the M operand and a tile's rows as N, a group's last
+// tile would cost what its rows cost; but tensor memory then holds y
+// transposed, and turning it around through shared memory took more than the
+// padding: 64 groups of 512 rows, 4096 x 2048, 157 us against 134.)
 //
 // Roles (10 warps per CTA): 0-7 epilogue (tensor-memory lane quarter warp % 4,
 // column half warp / 4), 8 TMA producer, 9 MMA issuer (CTA 0 only).  Barriers:
@@ -34,32 +40,39 @@ namespace svdq {
 namespace {
 
 constexpr int BM = 128;                            // rows per CTA
-constexpr int BN = 256;                            // weight rows per tile
-constexpr int BN_HALF = BN / 2;
 constexpr int BK_BYTES = 128;                      // 256 elements of K per stage
-constexpr int STAGES = 5;
 constexpr int A_BYTES = BM * BK_BYTES;
-constexpr int B_BYTES = BN_HALF * BK_BYTES;
 constexpr int SF_BYTES = 1024;                     // 128 rows x 256 columns of scales
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 3 * SF_BYTES;   // 35 KB
-static_assert(STAGE_BYTES % 1024 == 0, "stages keep the 1024-byte alignment of SWIZZLE_128B");
 constexpr int EPI_WARPS = 8;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;
 constexpr int NUM_THREADS = 10 * 32;
-constexpr int EPI_COLS = BN / 2;                   // accumulator columns per epilogue warp
-constexpr int EPI_CHUNK = 32;                      // columns per TMA store
-constexpr int EPI_BUF_BYTES = 32 * EPI_CHUNK * 2;
-constexpr int EPI_BYTES = EPI_WARPS * 2 * EPI_BUF_BYTES;
+constexpr int EPI_BUF_BYTES = 32 * 32 * 2;         // 32 rows x 32 columns of output
 constexpr int TMEM_COLS = 512;
-constexpr int SF_COLS = 24;                        // SFA 8 + SFB 16 columns per stage
-constexpr int TMEM_SF0 = BN;
-static_assert(TMEM_SF0 + STAGES * SF_COLS <= TMEM_COLS, "one scale buffer per stage above the accumulator");
 constexpr uint16_t PAIR_MASK = 0x3;
 constexpr unsigned long long kDrainLimitNs = 2000000000ull;
 
+template <int kParts>
+struct Cfg {
+  static constexpr int kPart = kMxPairCols<kParts> / kParts;               // weight rows of a part (MMA N)
+  static constexpr int kCols = kParts * kPart;
+  static constexpr int kPartBytes = kPart / 2 * BK_BYTES;                  // a CTA's half of a part
+  static constexpr int kSfOff = A_BYTES + kParts * kPartBytes;             // SFA, then the tile's SFB blocks
+  static constexpr int kBlocks = kCols / 128;
+  static constexpr int kStageBytes = kSfOff + (1 + kBlocks) * SF_BYTES;    // 35 or 44 KB
+  static constexpr int kStages = kParts == 1 ? 5 : 4;
+  static constexpr int kWarpCols = kCols / 2;                              // accumulator columns per epilogue warp
+  static constexpr int kBiasBytes = EPI_WARPS * kWarpCols * 4;
+  static constexpr int kEpiBytes = EPI_WARPS * 2 * EPI_BUF_BYTES + kBiasBytes;
+  static constexpr int kSfCols = 8 + 8 * kBlocks;                          // per stage
+  static constexpr int kTmemSf = kCols;
+  static_assert(kStageBytes % 1024 == 0 && kPartBytes % 1024 == 0, "SWIZZLE_128B tiles stay 1024-byte aligned");
+  static_assert(kTmemSf + kStages * kSfCols <= TMEM_COLS, "one scale buffer per stage above the accumulator");
+};
+
+template <int kParts>
 struct Ctl {
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
+  uint64_t full[Cfg<kParts>::kStages];
+  uint64_t empty[Cfg<kParts>::kStages];
   uint64_t acc_full;
   uint64_t acc_empty;
   uint64_t drain;
@@ -67,18 +80,23 @@ struct Ctl {
   int abort_flag;
   MxSched sched;
 };
-constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + sizeof(Ctl);
-static_assert(kSmemBytes <= 232448, "fits the 227 KB opt-in shared memory of one CTA");
+template <int kParts>
+constexpr int smem_bytes() {
+  return 1024 + Cfg<kParts>::kStages * Cfg<kParts>::kStageBytes + Cfg<kParts>::kEpiBytes + (int)sizeof(Ctl<kParts>);
+}
+static_assert(smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "fits the shared memory of one CTA");
 
-template <bool kGlu>
+template <int kParts>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     mxfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                            const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfw,
                            const __grid_constant__ CUtensorMap tm_y, const MxGemmParams p) {
+  using C = Cfg<kParts>;
+  constexpr int STAGES = C::kStages, STAGE_BYTES = C::kStageBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const epi_base = smem + STAGES * STAGE_BYTES;
-  Ctl* const ctl = reinterpret_cast<Ctl*>(epi_base + EPI_BYTES);
+  Ctl<kParts>* const ctl = reinterpret_cast<Ctl<kParts>*>(epi_base + C::kEpiBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();     // 0: leader (issues the MMAs), 1: peer
   const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
@@ -101,7 +119,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_sfa);
     prefetch_tmap(&tm_sfw);
-    if (!kGlu) prefetch_tmap(&tm_y);
+    prefetch_tmap(&tm_y);
   }
   if (warp == MMA_WARP) {
     tmem_alloc_pair(smem_u32(&ctl->tmem_base), TMEM_COLS);
@@ -120,8 +138,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const MxSched* const sched = &ctl->sched;
   const int groups = p.groups == 0 ? 1 : p.groups;
   const int k_slices = (p.K + 255) / 256, k_chunks = (p.K + 127) / 128;
-  constexpr int kTileCols = kGlu ? BN_HALF : BN;             // output columns per tile
-  const int tiles_n = (p.N + kTileCols - 1) / kTileCols;
+  const int tiles_n = (p.N + C::kCols - 1) / C::kCols;
   const int blocks_n = (p.N + 127) / 128;                    // 128-row scale blocks of one weight matrix
   const int num_tiles = sched->pre[groups] * tiles_n;
   const WaitCtx wctx{&ctl->abort_flag, p.dev_status, p.timeout_ns};
@@ -136,28 +153,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, 2 * BM, e);
       const int row0 = t.row0 + (int)rank * BM;
       const int block_a = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + 2 * t.mt + (int)rank;
-      // Weight rows and scale blocks: SwiGLU's tile takes the same 128 rows of
-      // the group's two matrices.
-      const int row_w = kGlu ? (2 * t.e + (int)rank) * p.N + t.nt * BN_HALF
-                             : t.e * p.N + t.nt * BN + (int)rank * BN_HALF;
-      const int block_w0 = kGlu ? 2 * t.e * blocks_n + t.nt : t.e * blocks_n + 2 * t.nt;
-      const int block_w1 = kGlu ? block_w0 + blocks_n : block_w0 + 1;
+      const int row_w = t.e * p.N + t.nt * C::kCols + (int)rank * (C::kPart / 2);
+      const int block_w = t.e * blocks_n + t.nt * C::kBlocks;
       for (int kb = 0; kb < k_slices; ++kb) {
         if (!mbar_wait_warp(smem_u32(&ctl->empty[stage]), phase ^ 1, wctx, kDevTimeoutProducer)) {
           ok = false;
           break;
         }
         if (elect_one()) {
-          const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_BYTES, sf = sb + B_BYTES;
+          const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_BYTES, sf = sa + C::kSfOff;
           const uint32_t local = smem_u32(&ctl->full[stage]);
           const uint32_t full = rank == 0 ? local : mapa_shared(local, 0);
           if (rank == 0) mbar_arrive_expect_tx(local, 2 * STAGE_BYTES);
-          tma_load_2d_pair(sb, &tm_w, kb * BK_BYTES, row_w, full, pol);
+#pragma unroll
+          for (int i = 0; i < kParts; ++i)
+            tma_load_2d_pair(sb + i * C::kPartBytes, &tm_w, kb * BK_BYTES, row_w + i * C::kPart, full, pol);
           tma_load_2d_pair(sa, &tm_a, kb * BK_BYTES, row0, full, pol);
           // Scales: 256-byte rows, four per 128-row block and slice.
           tma_load_2d_pair(sf, &tm_sfa, 0, (block_a * k_chunks + 2 * kb) * 2, full, pol);
-          tma_load_2d_pair(sf + SF_BYTES, &tm_sfw, 0, (block_w0 * k_chunks + 2 * kb) * 2, full, pol);
-          tma_load_2d_pair(sf + 2 * SF_BYTES, &tm_sfw, 0, (block_w1 * k_chunks + 2 * kb) * 2, full, pol);
+#pragma unroll
+          for (int i = 0; i < C::kBlocks; ++i)
+            tma_load_2d_pair(sf + (1 + i) * SF_BYTES, &tm_sfw, 0, ((block_w + i) * k_chunks + 2 * kb) * 2, full, pol);
         }
         __syncwarp();
         issued_mask |= 1u << stage;
@@ -183,7 +199,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      const uint32_t idesc0 = mx_idesc(2 * BM, BN, 0), idesc1 = mx_idesc(2 * BM, BN, 1);
+      const uint32_t idesc0 = mx_idesc(2 * BM, C::kPart, 0), idesc1 = mx_idesc(2 * BM, C::kPart, 1);
       for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
         // Both CTAs' epilogues have taken the previous tile's accumulator.
         if (!mbar_wait_warp(smem_u32(&ctl->acc_empty), acc_phase ^ 1, wctx, kDevTimeoutMma)) break;
@@ -195,24 +211,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_BYTES, ssf = sb + B_BYTES;
-            const uint32_t sf = tmem + TMEM_SF0 + stage * SF_COLS;
+            const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), ssf = sa + C::kSfOff;
+            const uint32_t sf = tmem + C::kTmemSf + stage * C::kSfCols;
             // 64-column steps of this slice, and the 128-column scale tiles they read.
             const int steps = min(4, (p.K - kb * 256 + 63) / 64);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               if (2 * j < steps) {
                 tmem_cp_pair_32x128_warpx4(sf + 4 * j, mx_scale_desc(ssf + 512 * j));
-                tmem_cp_pair_32x128_warpx4(sf + 8 + 8 * j, mx_scale_desc(ssf + SF_BYTES + 512 * j));
-                tmem_cp_pair_32x128_warpx4(sf + 12 + 8 * j, mx_scale_desc(ssf + 2 * SF_BYTES + 512 * j));
+#pragma unroll
+                for (int i = 0; i < C::kBlocks; ++i)
+                  tmem_cp_pair_32x128_warpx4(sf + 8 + 4 * C::kBlocks * j + 4 * i,
+                                             mx_scale_desc(ssf + (1 + i) * SF_BYTES + 512 * j));
               }
             }
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              if (s < steps)
-                mma_mxfp4_pair(tmem, mx_operand_desc(sa + 32 * s), mx_operand_desc(sb + 32 * s),
-                               s & 1 ? idesc1 : idesc0, sf + 4 * (s >> 1), sf + 8 + 8 * (s >> 1),
-                               kb > 0 || s > 0 ? 1u : 0u);
+#pragma unroll
+              for (int i = 0; i < kParts; ++i)
+                if (s < steps)
+                  mma_mxfp4_pair(tmem + i * C::kPart, mx_operand_desc(sa + 32 * s),
+                                 mx_operand_desc(sa + A_BYTES + i * C::kPartBytes + 32 * s), s & 1 ? idesc1 : idesc0,
+                                 sf + 4 * (s >> 1), sf + 8 + 4 * C::kBlocks * (s >> 1) + i * (C::kPart / 32),
+                                 kb > 0 || s > 0 ? 1u : 0u);
             // Both CTAs may refill this stage once the MMAs reading it are done.
             tc_commit_pair_mc(smem_u32(&ctl->empty[stage]), PAIR_MASK);
           }
@@ -236,14 +257,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
-    // A warp pulls its 32 rows x 128 columns with four loads and one wait,
-    // releases the accumulator (remotely for CTA 1) and only then computes.
+    // A warp adds the bias and rounds to 16 bits as it loads its 32 rows x
+    // half of the columns, releases the accumulator (remotely for CTA 1) and
+    // only then stores.
     const int q = warp & 3, h = warp >> 2;
     const bool fp16 = p.fp16 != 0;
     uint8_t* const buf0 = epi_base + warp * 2 * EPI_BUF_BYTES;
+    float* const bias_tab = reinterpret_cast<float*>(epi_base + EPI_WARPS * 2 * EPI_BUF_BYTES) + warp * C::kWarpCols;
     const uint32_t acc_empty_local = smem_u32(&ctl->acc_empty);
     const uint32_t acc_empty_leader = rank == 0 ? acc_empty_local : mapa_shared(acc_empty_local, 0);
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(h * C::kWarpCols);
     uint32_t acc_phase = 0;
     int store_seq = 0, e = 0;
     for (int tile = pair; tile < num_tiles; tile += num_pairs) {
@@ -251,35 +274,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int slab = (int)rank * BM + 32 * q;        // the warp's first row within the tile
       const int valid = min(32, t.rows - slab);        // its rows inside the group (may be <= 0)
       const int row0 = t.row0 + slab;
-      // Plain: the warp's 128 columns of y.  SwiGLU: its 64 hidden columns.
-      const int nw = t.nt * kTileCols + h * (kTileCols / 2);
-      // Lane l holds the bias of plain columns nw + 4 l .. + 3, or of hidden
-      // columns nw + 2 l, + 1 for both factors.
-      uint2 bias4 = make_uint2(0, 0);
+      const int nw = t.nt * C::kCols + h * C::kWarpCols;
       if (p.bias != nullptr) {
-        if constexpr (kGlu) {
-          if (nw + 2 * lane < p.N) {
-            const uint16_t* b = p.bias + (size_t)t.e * 2 * p.N + nw + 2 * lane;
-            bias4 = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(b)),
-                               __ldg(reinterpret_cast<const uint32_t*>(b + p.N)));
-          }
-        } else if (nw + 4 * lane < p.N) {
-          bias4 = __ldg(reinterpret_cast<const uint2*>(p.bias + (size_t)t.e * p.N + nw) + lane);
+#pragma unroll
+        for (int i = 0; i < C::kWarpCols / 32; ++i) {
+          const int n = nw + 32 * i + lane;
+          bias_tab[32 * i + lane] = n < p.N ? mx_load16(p.bias + (size_t)t.e * p.N + n, fp16) : 0.f;
         }
+        __syncwarp();
       }
       const bool got = mbar_wait(smem_u32(&ctl->acc_full), acc_phase, wctx, kDevTimeoutEpilogue);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
-      uint32_t r[4][32];
+      uint32_t out[C::kWarpCols / 32][16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = kGlu ? (i >> 1) * BN_HALF + h * 64 + (i & 1) * 32 : h * EPI_COLS + 32 * i;
-        tmem_ld_32x32b_x32(lane_base + (uint32_t)col, r[i]);
+      for (int i = 0; i < C::kWarpCols / 32; ++i) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(acc + 32 * i, r);
+        tmem_ld_wait(r);
+        if (p.bias != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 b = reinterpret_cast<const float4*>(bias_tab + 32 * i)[j];
+            const float2 lo = __fadd2_rn(make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])),
+                                         make_float2(b.x, b.y));
+            const float2 hi = __fadd2_rn(make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])),
+                                         make_float2(b.z, b.w));
+            out[i][2 * j] = mx_pack16(lo.x, lo.y, fp16);
+            out[i][2 * j + 1] = mx_pack16(hi.x, hi.y, fp16);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            out[i][j] = mx_pack16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), fp16);
+        }
       }
-      tmem_ld_wait(r[0]);
-      reg_fence(r[1]);
-      reg_fence(r[2]);
-      reg_fence(r[3]);
       // The loads are complete (wait::ld) and ordered before the arrive by
       // the tcgen05 fence, which is all the MMA warp needs: CTA 1's remote
       // arrive is relaxed.
@@ -293,89 +322,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       acc_phase ^= 1;
       if (valid <= 0) continue;
-      auto lo16 = [&](uint32_t w) {
-        return fp16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xFFFF))) : __uint_as_float(w << 16);
-      };
-      auto hi16 = [&](uint32_t w) {
-        return fp16 ? __half2float(__ushort_as_half((unsigned short)(w >> 16))) : __uint_as_float(w & 0xFFFF0000u);
-      };
-      if constexpr (kGlu) {
-        // r[0..1]: gate columns nw .. + 63, r[2..3]: the other factor's.  Each
-        // 32-column half is one block of the next product's K.
-        const int local = t.mt * 2 * BM + slab + lane;      // row within the group
-        const int block = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + local / 128;
-        uint8_t* const sc = p.h_scales + mx_tile_offset(block, blocks_n, t.nt) + (local & 31) * 16 +
-                            (local % 128) / 32 * 4 + 2 * h;
-        uint8_t* const codes = p.h_codes + (size_t)(row0 + lane) * (p.N / 2) + nw / 2;
-        uint32_t bytes = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const uint32_t bg = __shfl_sync(0xffffffffu, bias4.x, 16 * i + j / 2),
-                           bu = __shfl_sync(0xffffffffu, bias4.y, 16 * i + j / 2);
-            const float hv = mx_swiglu(__fadd_rn(__uint_as_float(r[i][j]), j & 1 ? hi16(bg) : lo16(bg)),
-                                       __fadd_rn(__uint_as_float(r[2 + i][j]), j & 1 ? hi16(bu) : lo16(bu)));
-            r[i][j] = __float_as_uint(hv);
-            top = max(top, r[i][j] & 0x7FFFFFFFu);
-          }
-          const uint32_t sb = mx_scale_byte(top);
-          const float inv = mx_inv_scale(sb);
-          uint32_t w[4];
+      for (int i = 0; i < C::kWarpCols / 32; ++i) {
+        const int ncol = nw + 32 * i;
+        if (valid == 32) {
+          uint8_t* const buf = buf0 + (store_seq & 1) * EPI_BUF_BYTES;
+          if (lane == 0) bulk_wait_read<1>();   // the store two pieces ago has read this buffer
+          __syncwarp();
+          uint8_t* const row = buf + lane * 64;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float2 v[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              v[x] = __fmul2_rn(make_float2(__uint_as_float(r[i][8 * j + 2 * x]),
-                                            __uint_as_float(r[i][8 * j + 2 * x + 1])),
-                                make_float2(inv, inv));
-            w[j] = sb == 255u ? 0u : mx_e2m1x8(v);
+            const int pj = j ^ ((lane >> 1) & 3);  // 64-byte swizzle
+            *reinterpret_cast<uint4*>(row + pj * 16) =
+                make_uint4(out[i][4 * j], out[i][4 * j + 1], out[i][4 * j + 2], out[i][4 * j + 3]);
           }
-          const bool in_n = nw + 32 * i < p.N;              // N % 32 == 0
-          bytes |= (in_n ? sb : 0u) << (8 * i);             // padding groups get byte 0
-          if (in_n && lane < valid) *reinterpret_cast<uint4*>(codes + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if (lane < valid) *reinterpret_cast<uint16_t*>(sc) = (uint16_t)bytes;
-      } else {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && ncol < p.N) tma_store_2d(&tm_y, ncol, row0, smem_u32(buf));
+          if (lane == 0) bulk_commit();
+          ++store_seq;
+        } else if (lane < valid) {
+          uint16_t* const y = p.y + (size_t)(row0 + lane) * p.ldy + ncol;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ncol = nw + 32 * i;
-          uint32_t packed[16];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t bx = __shfl_sync(0xffffffffu, bias4.x, 8 * i + j),
-                           by = __shfl_sync(0xffffffffu, bias4.y, 8 * i + j);
-            packed[2 * j] = mx_pack16(__fadd_rn(__uint_as_float(r[i][4 * j]), lo16(bx)),
-                                      __fadd_rn(__uint_as_float(r[i][4 * j + 1]), hi16(bx)), fp16);
-            packed[2 * j + 1] = mx_pack16(__fadd_rn(__uint_as_float(r[i][4 * j + 2]), lo16(by)),
-                                          __fadd_rn(__uint_as_float(r[i][4 * j + 3]), hi16(by)), fp16);
-          }
-          if (valid == 32) {
-            uint8_t* const buf = buf0 + (store_seq & 1) * EPI_BUF_BYTES;
-            if (lane == 0) bulk_wait_read<1>();   // the store two chunks ago has read this buffer
-            __syncwarp();
-            uint8_t* const row = buf + lane * 64;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int pj = j ^ ((lane >> 1) & 3);  // 64-byte swizzle
-              *reinterpret_cast<uint4*>(row + pj * 16) =
-                  make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && ncol < p.N) tma_store_2d(&tm_y, ncol, row0, smem_u32(buf));
-            if (lane == 0) bulk_commit();
-            ++store_seq;
-          } else if (lane < valid) {
-            uint16_t* const out = p.y + (size_t)(row0 + lane) * p.ldy + ncol;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (ncol + 8 * j < p.N)
-                *reinterpret_cast<uint4*>(out + 8 * j) =
-                    make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-          }
+          for (int j = 0; j < 4; ++j)
+            if (ncol + 8 * j < p.N)
+              *reinterpret_cast<uint4*>(y + 8 * j) =
+                  make_uint4(out[i][4 * j], out[i][4 * j + 1], out[i][4 * j + 2], out[i][4 * j + 3]);
         }
       }
     }
@@ -393,48 +365,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-template <bool kGlu>
+template <int kParts>
 cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, cudaStream_t stream, bool pdl) {
-  auto kernel = mxfp4_gemm_pair_kernel<kGlu>;
-  if (cudaError_t e = mx_allow_smem<mxfp4_gemm_pair_kernel<kGlu>>((int)kSmemBytes)) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(NUM_THREADS);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  int pairs = 0;
-  {
-    cfg.gridDim = dim3(2);
-    cfg.numAttrs = 1;
-    static MxPerDevice<int> cache;
-    if (cudaError_t e = cache.get(&pairs, [&](int* n) {
-          if (cudaError_t err = cudaOccupancyMaxActiveClusters(n, kernel, &cfg)) return err;
-          return *n < 1 ? cudaErrorInvalidConfiguration : cudaSuccess;
-        }))
-      return e;
-  }
-  constexpr int kTileCols = kGlu ? BN_HALF : BN;
-  const long long by_rows = ((long long)p.rows + 2 * BM - 1) / (2 * BM);
-  const long long m_tiles =
-      p.groups == 0 ? by_rows : std::min<long long>(p.rows, p.rows / (2 * BM) + (long long)p.groups);
-  const long long tiles = m_tiles * ((p.N + kTileCols - 1) / kTileCols);
-  cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(tiles, pairs)));
-  cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, t.act, t.w, t.sfa, t.sfw, t.y, p);
+  constexpr int kSmem = smem_bytes<kParts>(), kCols = Cfg<kParts>::kCols;
+  if (cudaError_t e = mx_allow_smem<mxfp4_gemm_pair_kernel<kParts>>(kSmem)) return e;
+  const long long m_tiles = p.groups == 0
+                                ? ((long long)p.rows + 2 * BM - 1) / (2 * BM)
+                                : std::min<long long>(p.rows, p.rows / (2 * BM) + (long long)p.groups);
+  return mx_launch_pairs<mxfp4_gemm_pair_kernel<kParts>, NUM_THREADS, kSmem>(
+      m_tiles * ((p.N + kCols - 1) / kCols), stream, pdl, t.act, t.w, t.sfa, t.sfw, t.y, p);
 }
 
 }  // namespace
 
-cudaError_t launch_mxfp4_gemm_pair(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, cudaStream_t stream,
+cudaError_t launch_mxfp4_gemm_pair(const MxGemmParams& p, const MxGemmTmaps& t, int parts, cudaStream_t stream,
                                    bool pdl) {
-  return swiglu ? launch_impl<true>(p, t, stream, pdl) : launch_impl<false>(p, t, stream, pdl);
+  return parts == 2 ? launch_impl<2>(p, t, stream, pdl) : launch_impl<1>(p, t, stream, pdl);
 }
 
 }  // namespace svdq

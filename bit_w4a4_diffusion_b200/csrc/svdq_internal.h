@@ -303,9 +303,15 @@ struct MxGemmParams {
 struct MxGemmTmaps {
   CUtensorMap act, w, sfa, sfw, y;
 };
-// 256 x 256 tiles on CTA pairs (SwiGLU: 256 rows x 128 hidden columns).
-cudaError_t launch_mxfp4_gemm_pair(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, cudaStream_t stream,
+// CTA pairs: 256 rows x kMxPairCols<parts> weight rows, t.w in boxes of half a
+// part (kMxPairCols<parts> / parts / 2 rows); SwiGLU: 256 rows x 128 hidden
+// columns, t.w in boxes of 128 rows.  t.act in boxes of 128 rows.
+template <int kParts>
+constexpr int kMxPairCols = kParts == 1 ? 256 : 384;
+cudaError_t launch_mxfp4_gemm_pair(const MxGemmParams& p, const MxGemmTmaps& t, int parts, cudaStream_t stream,
                                    bool pdl);
+cudaError_t launch_mxfp4_gemm_pair_swiglu(const MxGemmParams& p, const MxGemmTmaps& t, cudaStream_t stream,
+                                          bool pdl);
 // 128 weight rows x up to 64 rows per CTA, the weight as the M operand;
 // t.act's box is kMxNarrowBox rows.
 constexpr int kMxNarrowBox = 32;
@@ -343,6 +349,36 @@ cudaError_t mx_allow_smem(int bytes) {
     *n = bytes;
     return cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   });
+}
+
+// Launches a CTA-pair kernel (clusters of two) on as many pairs as there are
+// tiles or as fit the device at once.
+template <auto kKernel, int kThreads, int kSmem, class... Args>
+cudaError_t mx_launch_pairs(long long tiles, cudaStream_t stream, bool pdl, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  static MxPerDevice<int> fit;
+  int pairs = 0;
+  cfg.gridDim = dim3(2);
+  cfg.numAttrs = 1;
+  if (cudaError_t e = fit.get(&pairs, [&](int* n) {
+        if (cudaError_t err = cudaOccupancyMaxActiveClusters(n, kKernel, &cfg)) return err;
+        return *n < 1 ? cudaErrorInvalidConfiguration : cudaSuccess;
+      }))
+    return e;
+  cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(tiles, pairs)));
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kKernel, args...);
 }
 
 // What the entry points of other files share with abi.cu: the device check

@@ -115,6 +115,7 @@ GROUPS = {   # offsets, rows (the capacity)
     "first and last rows of no group": ([7, 40, 40, 300], 345),
     "all empty": ([9, 9, 9], 20),
     "long": ([0, 1, 700, 701, 1300], 1300),
+    "around the tiles": ([0, 383, 767, 1152, 1408, 1408, 1665, 2434], 2440),
 }
 
 
@@ -181,7 +182,8 @@ def dense_case(M, N, K, dtype, with_bias, seed, device="cuda"):
     (1, 8, 32), (1, 1024, 2048), (2, 136, 96), (15, 24, 64), (16, 128, 256), (17, 520, 160), (31, 200, 320),
     (32, 128, 288), (33, 392, 512), (64, 1000, 1056), (65, 256, 768), (97, 128, 544), (127, 520, 224),
     (128, 256, 4096), (129, 264, 640), (200, 128, 6400), (255, 304, 96), (256, 256, 256), (257, 520, 352),
-    (600, 1304, 512), (1030, 2056, 1024),
+    (272, 136, 96), (384, 256, 2048), (385, 512, 288), (512, 264, 64), (600, 1304, 512), (769, 384, 1312),
+    (1030, 2056, 1024), (1153, 128, 256), (2900, 1032, 320),
 ])
 def test_gemm_exact(monkeypatch, kernel, M, N, K):
     pick(monkeypatch, kernel)
