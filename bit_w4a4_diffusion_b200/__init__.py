@@ -168,6 +168,9 @@ def check_device_status(stream=None):
     """Raise SvdqError(5) if a call made with ``dev_status=None`` timed out on
     the device since the last check (the word is cleared either way)."""
     code = device_status(clear=True, stream=stream)
+    if code == 5:
+        raise SvdqError(5, "row offsets or row indices of an MXFP4 call were out of range (code 5); its outputs are "
+                           "not valid")
     if code != 0:
         raise SvdqError(5, f"a device-side wait gave up (code {code}); outputs of the calls since the last "
                            "check are not valid")

@@ -294,6 +294,25 @@ SVDQ_DEV void mma_mxfp4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, ui
 SVDQ_DEV uint64_t mx_operand_desc(uint32_t saddr) { return smem_desc(saddr, 16, 1024, 2); }
 SVDQ_DEV uint64_t mx_scale_desc(uint32_t saddr) { return smem_desc(saddr, 0, 128, 0); }
 
+// ------------------------------------------------------------------ the end of a pair
+// After a wait that gave up in either CTA of a pair, loads into the peer's
+// shared memory may still be on their way, counted on a barrier that nobody
+// reads any more.  Each warp tells the peer of an abort before the pair's last
+// barrier, and after it both CTAs stay for as long as such loads can take.
+SVDQ_DEV void mx_pair_meet(int* abort_flag, uint32_t rank) {
+  if (*reinterpret_cast<volatile int*>(abort_flag) != 0)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(abort_flag), rank ^ 1u)), "r"(1)
+                 : "memory");
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (*reinterpret_cast<volatile int*>(abort_flag) != 0) {
+    constexpr uint64_t kStayNs = 200000;
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kStayNs) __nanosleep(1000);
+  }
+}
+
 // ------------------------------------------------------------------ outputs
 SVDQ_DEV float mx_load16(const uint16_t* p, bool fp16) {
   const uint16_t b = __ldg(p);

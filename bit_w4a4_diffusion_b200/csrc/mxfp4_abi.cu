@@ -136,8 +136,14 @@ long long narrow_m_tiles(int groups, int rows) {
                      : std::min<long long>(rows, rows / kMxNarrowRows + (long long)groups);
 }
 
-// Which kernel a product takes.  SVDQ_MXFP4_GEMM_KERNEL=pair or =narrow (read
-// at every call) forces one of them.  Otherwise the narrow kernel while its
+// SVDQ_MXFP4_GEMM_KERNEL (read at every call) forces a kernel: "narrow",
+// "pair", or "pair256" / "pair384" for the pair kernel with tiles of that width.
+bool forced(const char* name, size_t n) {
+  const char* v = getenv("SVDQ_MXFP4_GEMM_KERNEL");
+  return v && strncmp(v, name, n) == 0;
+}
+
+// Which kernel a product takes, unless one is forced.  The narrow kernel while its
 // tiles fit the chip's CTA slots once, or while a group has so few rows on
 // average that the weight bytes dominate.  GPU time narrow / pair, us:
 //   dense, 4096 x 4096: M = 64 6.6 / 10.4, 512 9.9 / 11.0, 768 15.5 / 11.7;
@@ -145,9 +151,8 @@ long long narrow_m_tiles(int groups, int rows) {
 //   32 groups, 2048 x 2048, rows each: 96 21.9 / 22.2, 128 25.8 / 24.3
 //   SwiGLU, the same: 96 34.9 / 36.4, 128 36.7 / 36.7, 160 44.5 / 36.9
 bool use_pair(int groups, int rows, int N, bool swiglu, int sms) {
-  const char* v = getenv("SVDQ_MXFP4_GEMM_KERNEL");
-  if (v && strcmp(v, "pair") == 0) return true;
-  if (v && strcmp(v, "narrow") == 0) return false;
+  if (forced("pair", 4)) return true;
+  if (forced("narrow", 6)) return false;
   if (narrow_m_tiles(groups, rows) * ((N + 127) / 128) <= (long long)kMxNarrowPerSm * sms) return false;
   return rows / (groups == 0 ? 1 : groups) > (swiglu ? 128 : 96);
 }
@@ -173,6 +178,8 @@ int choose_splits(long long tiles, int K, bool swiglu, int sms) {
 // 809 cycles, a tile's end 1400 or 2100.  1 / 2, us: 8192^3 186.9 / 184.3;
 // 4096 x 12288 x 4096 79.3 / 74.1; 16 groups of 1024, 4096 x 2048 73.1 / 70.4.
 int choose_parts(int groups, int rows, int N, int K, int sms) {
+  if (forced("pair256", 7)) return 1;
+  if (forced("pair384", 7)) return 2;
   const double slices = (K + 255) / 256, pairs = sms / 2;
   auto cycles = [&](int cols, double slice, double end) {
     // Groups end anywhere: half a tile more for each.
@@ -265,7 +272,7 @@ int check_input(int dtype, int rows, int K, const void* x, long long ldx, const 
   if (!aligned(row_index, 4)) return record_error(SVDQ_ERR_INVALID_ARG, "row_index must be 4-byte aligned");
   if (x_rows < 0 || (!row_index && x_rows < rows))
     return record_error(SVDQ_ERR_INVALID_ARG, "x has %d rows, %d are asked for", x_rows, rows);
-  return check_grid(scale_blocks(kMxMaxGroups, rows) * ((K + 255) / 256), "quantize");
+  return check_grid(scale_blocks(kMxMaxGroups, rows) * ((K + 255) / 256) * kMxRowCtas, "quantize");
 }
 
 int check_workspace(const void* ws, long long have, long long need) {
@@ -352,7 +359,7 @@ int mxfp4_dequantize(int dtype, int rows, int K, const void* codes, const void* 
   if (dtype != kMxBf16 && dtype != kMxFp32)
     return record_error(SVDQ_ERR_INVALID_ARG, "dtype %d is not MXFP4_BF16 or MXFP4_FP32", dtype);
   if (rows == 0) return SVDQ_OK;
-  if (int s = check_grid(scale_blocks(kMxMaxGroups, rows) * ((K + 255) / 256), "dequantize")) return s;
+  if (int s = check_grid(scale_blocks(kMxMaxGroups, rows) * ((K + 255) / 256) * kMxRowCtas, "dequantize")) return s;
   if (int s = check_buffer(codes, "codes")) return s;
   if (int s = check_buffer(scales, "scales")) return s;
   if (int s = check_matrix(out, ldo, K, elem_size(dtype), "out")) return s;

@@ -404,6 +404,9 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
           if (lane == 0) mbar_arrive(smem_u32(&ctl->full[stage]));
         }
       }
+      // After a wait that gave up: complete the stage's barrier, on which the
+      // producer waits for its own copies.
+      if (!ok && lane == 0) mbar_arrive(smem_u32(&ctl->full[stage]));
     }
   } else {
     // -------------------------------------------------------------- epilogue

@@ -317,9 +317,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   // Both CTAs leave together: CTA 0's MMAs write CTA 1's tensor memory, and
   // CTA 1's loads count on CTA 0's barriers.
-  __syncwarp();
-  tc_fence_before();
-  cluster_sync();
+  mx_pair_meet(&ctl->abort_flag, rank);
   if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, TMEM_COLS);

@@ -329,6 +329,7 @@ cudaError_t launch_rows(const P& p, cudaStream_t stream, bool pdl) {
   const int k_slices = (p.K + MQ_COLS - 1) / MQ_COLS;
   const long long tiles = row_blocks(p.rows, p.groups) * k_slices;
   const int spread = tiles < MQ_FEW_TILES;
+  static_assert(32 / kWarps <= kMxRowCtas, "the entry points check the grid's size");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * (32 / (kWarps * MQ_UNITS)) * (spread ? MQ_UNITS : 1)));
   cfg.blockDim = dim3(kWarps * 32);

@@ -261,6 +261,7 @@ struct MxQuantParams {
   uint8_t* scales;        // tiled E8M0
   int* dev_status;
 };
+constexpr int kMxRowCtas = 8;   // CTAs per 128 rows x 256 columns, at most
 cudaError_t launch_mxfp4_quantize(const MxQuantParams& p, cudaStream_t stream, bool pdl);
 
 struct MxDequantParams {

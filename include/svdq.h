@@ -478,12 +478,13 @@ int mxfp4_dequantize(int dtype, int rows, int K, const void* codes, const void* 
  * mxfp4_linear, mxfp4_grouped_linear: mxfp4_quantize of x, then the product,
  * on `stream`; workspace of mxfp4_workspace_bytes, which calls may share only
  * if they do not overlap in time.
- * The product runs on one of two kernels: 256 x 256 tiles on CTA pairs, or,
- * with few rows per group, a weight stream with the rows as the narrow
- * operand; the linear calls with up to MXFP4_FUSED_ROWS (grouped:
- * MXFP4_FUSED_GROUPED_ROWS) rows are one launch of the latter, with the
- * quantizer inside.  SVDQ_MXFP4_GEMM_KERNEL=pair or =narrow in the environment (read
- * at every call) forces one; they differ in the order of fp32 sums. */
+ * The product runs on one of two kernels: tiles of 256 rows x 256 or 384
+ * columns on CTA pairs, or, with few rows per group, a weight stream with the
+ * rows as the narrow operand; the linear calls with up to MXFP4_FUSED_ROWS
+ * (grouped: MXFP4_FUSED_GROUPED_ROWS) rows are one launch of the latter, with
+ * the quantizer inside.  SVDQ_MXFP4_GEMM_KERNEL=pair, pair256, pair384 or
+ * narrow in the environment (read at every call) forces one for larger calls;
+ * they differ in the order of fp32 sums. */
 int mxfp4_gemm(int dtype, int M, int N, int K, const void* act_codes, const void* act_scales, const void* w_codes,
                const void* w_scales, const void* bias, void* y, long long ldy, int* dev_status, void* stream);
 int mxfp4_grouped_gemm(int dtype, int groups, int rows, int N, int K, const int* offsets, const void* act_codes,

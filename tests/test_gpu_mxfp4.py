@@ -17,7 +17,7 @@ from tests.helpers import nibbles
 
 pytestmark = pytest.mark.gpu
 
-KERNELS = ["pair", "narrow", None]
+KERNELS = ["pair256", "pair384", "narrow", None]
 DTYPES = [torch.bfloat16, torch.float16]
 
 
@@ -192,7 +192,7 @@ def test_gemm_exact(monkeypatch, kernel, M, N, K):
         same_bits(B.mxfp4_gemm(a, sa, w, bias=b, dtype=dtype), want)
 
 
-@pytest.mark.parametrize("kernel", ["pair", "narrow"])
+@pytest.mark.parametrize("kernel", ["pair256", "pair384", "narrow"])
 @pytest.mark.parametrize("M,N", [(1, 72), (40, 136), (129, 72), (300, 264)])
 def test_gemm_writes_only_y(monkeypatch, kernel, M, N):
     """y as a window of a larger matrix: the rows and columns around it stay."""
@@ -206,7 +206,7 @@ def test_gemm_writes_only_y(monkeypatch, kernel, M, N):
     assert (big == 3.0).all()
 
 
-@pytest.mark.parametrize("kernel", ["pair", "narrow"])
+@pytest.mark.parametrize("kernel", ["pair256", "pair384", "narrow"])
 def test_gemm_every_code_pair(monkeypatch, kernel):
     """One-element rows: every pair of E2M1 codes at every place of a block,
     scales over a wide range, gives the exact product."""
@@ -226,7 +226,7 @@ def test_gemm_every_code_pair(monkeypatch, kernel):
     same_bits(y.double(), torch.from_numpy(want))      # at most 6 significant bits: exact in bf16
 
 
-@pytest.mark.parametrize("kernel", ["pair", "narrow"])
+@pytest.mark.parametrize("kernel", ["pair256", "pair384", "narrow"])
 def test_nan_and_infinity_reach_only_their_rows_and_columns(monkeypatch, kernel):
     pick(monkeypatch, kernel)
     rng = np.random.default_rng(9)
@@ -491,9 +491,11 @@ def test_swiglu_quant(monkeypatch, kernel, name, width, K):
         assert flips < 1e-3 and scale_flips < 1e-3
 
 
-def test_swiglu_quant_of_nan_and_large_values():
+@pytest.mark.parametrize("kernel", ["pair256", "pair384", "narrow"])
+def test_swiglu_quant_of_nan_and_large_values(monkeypatch, kernel):
     """A NaN block in x makes its row's hidden blocks NaN (byte 255, codes 0);
     a gate of a few hundred either way gives 0 or the other factor."""
+    pick(monkeypatch, kernel)
     rng = np.random.default_rng(2)
     K, width = 64, 64
     x = rng.standard_normal((6, K)).astype(np.float32)
@@ -584,6 +586,30 @@ def test_experts_layer(T):
     z = B.mxfp4_linear(out.to(torch.bfloat16), B.to_device(B.mxfp4_pack_weights(
         F.bf16_bits(np.eye(K, dtype=np.float32)))))
     same_bits(z.double(), torch.from_numpy(O.values(*O.quantize(out.to(torch.bfloat16).cpu().double().numpy()))))
+
+
+# -------------------------------------------------------------- large sizes --
+
+def test_offsets_beyond_32_bits():
+    """Matrices of more than 2^32 elements: rows at the end equal those of a
+    small call."""
+    M, K = 66000, 65536 + 32
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    tail = C.rows(np.random.default_rng(1), 200, K, torch.bfloat16).cuda()
+    x[-200:] = tail
+    codes, scales = B.mxfp4_quantize(x)
+    want_c, want_s = B.mxfp4_quantize(tail)
+    assert torch.equal(codes[-200:], want_c)
+    v = B.mxfp4_dequantize(codes, scales, out=x)
+    assert v is x
+    same_bits(x[-200:].cpu(), B.mxfp4_dequantize(want_c, want_s).cpu())
+    del x, codes, scales, v
+    N, K = 66048, 64
+    x = C.rows(np.random.default_rng(2), M, K, torch.bfloat16).cuda()
+    w, _ = C.weight(np.random.default_rng(3), (), N, K, 0)
+    y = B.mxfp4_linear(x, w)
+    same_bits(y[-300:, -520:].cpu(), B.mxfp4_linear(x[-300:], w)[:, -520:].cpu())
+    same_bits(y[:300, :520].cpu(), B.mxfp4_linear(x[:300], w)[:, :520].cpu())
 
 
 # ------------------------------------------------- streams, graphs, threads --
@@ -724,6 +750,52 @@ def test_pdl_off_gives_the_same(monkeypatch):
     want = B.mxfp4_grouped_mlp_swiglu(x, off, up, down)
     monkeypatch.setenv("SVDQ_PDL", "0")
     same_bits(B.mxfp4_grouped_mlp_swiglu(x, off, up, down), want)
+
+
+def timed_out(call, status):
+    """Runs ``call`` with a wait limit of 1 ns and returns the status code."""
+    old = B.get_timeout_ns()
+    try:
+        B.set_timeout_ns(1)
+        call()
+        torch.cuda.synchronize()
+    finally:
+        B.set_timeout_ns(old)
+    code = int(status)
+    status.zero_()
+    return code
+
+
+@pytest.mark.parametrize("kernel,M,N,K", [("pair256", 600, 1024, 65536), ("pair384", 600, 768, 65536),
+                                          ("narrow", 700, 8200, 16384), ("narrow", 30, 512, 131072),
+                                          (None, 1, 40008, 16384), (None, 2, 1024, 131072)])
+def test_a_wait_that_gives_up_is_reported(monkeypatch, kernel, M, N, K):
+    """Every kernel, also with K split over a cluster and with the quantizer
+    inside, reports a wait that gave up and leaves the library usable.  The
+    clock is read every 64 polls, a few microseconds apart, so K is so long
+    that the epilogue waits tens of them for its first tile."""
+    pick(monkeypatch, kernel)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = C.rows(np.random.default_rng(M), M, K, torch.bfloat16).cuda()
+    w = {"codes": torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=g),
+         "scales": torch.randint(110, 118, (B.mxfp4_scale_bytes(N, K),), dtype=torch.uint8, device="cuda",
+                                 generator=g), "N": N, "K": K}
+    want = steps_linear(x, w)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert timed_out(lambda: B.mxfp4_linear(x, w, dev_status=status), status) in (1, 2, 3, 4)
+    same_bits(B.mxfp4_linear(x, w, dev_status=status), want)
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("kernel,T", [("pair", 3000), ("narrow", 3000), (None, 12)])
+def test_a_wait_that_gives_up_in_the_mlp_is_reported(monkeypatch, kernel, T):
+    pick(monkeypatch, kernel)
+    x, off, up, down = layer_set(3, T=T, E=2, K=32768, width=256)
+    want = B.mxfp4_grouped_mlp_swiglu(x, off, up, down)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert timed_out(lambda: B.mxfp4_grouped_mlp_swiglu(x, off, up, down, dev_status=status), status) in (1, 2, 3, 4)
+    same_bits(B.mxfp4_grouped_mlp_swiglu(x, off, up, down, dev_status=status), want)
+    assert int(status) == 0
 
 
 def test_no_rows():
