@@ -61,7 +61,8 @@ struct Ctl {
   int abort_flag;
   MxSched sched;
 };
-constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + sizeof(Ctl);
+constexpr int BIAS_BYTES = EPI_WARPS * 2 * 64 * 4;  // per epilogue warp: 64 hidden columns of both factors, fp32
+constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + BIAS_BYTES + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "fits the 227 KB opt-in shared memory of one CTA");
 
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -70,7 +71,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                            const MxGemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ctl* const ctl = reinterpret_cast<Ctl*>(smem + STAGES * STAGE_BYTES);
+  float* const bias_base = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);
+  Ctl* const ctl = reinterpret_cast<Ctl*>(smem + STAGES * STAGE_BYTES + BIAS_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();     // 0: leader (issues the MMAs), 1: peer
   const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
@@ -229,6 +231,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t acc_empty_local = smem_u32(&ctl->acc_empty);
     const uint32_t acc_empty_leader = rank == 0 ? acc_empty_local : mapa_shared(acc_empty_local, 0);
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+    float* const bias_tab = bias_base + warp * 128;      // gate 64, other 64
     uint32_t acc_phase = 0;
     int e = 0;
     for (int tile = pair; tile < num_tiles; tile += num_pairs) {
@@ -237,11 +240,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int valid = min(32, t.rows - slab);        // its rows inside the group (may be <= 0)
       const int row0 = t.row0 + slab;
       const int nw = t.nt * BN_HALF + h * 64;          // the warp's 64 hidden columns
-      // Lane l holds the biases of columns nw + 2 l, + 1 for both factors.
-      uint2 bias4 = make_uint2(0, 0);
-      if (p.bias != nullptr && nw + 2 * lane < p.N) {
-        const uint16_t* b = p.bias + (size_t)t.e * 2 * p.N + nw + 2 * lane;
-        bias4 = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(b)), __ldg(reinterpret_cast<const uint32_t*>(b + p.N)));
+      if (p.bias != nullptr) {
+        __syncwarp();   // the reads for the tile before are done
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = nw + 32 * (i & 1) + lane;
+          bias_tab[32 * i + lane] = n < p.N ? mx_load16(p.bias + ((size_t)t.e * 2 + (i >> 1)) * p.N + n, fp16) : 0.f;
+        }
+        __syncwarp();
       }
       const bool got = mbar_wait(smem_u32(&ctl->acc_full), acc_phase, wctx, kDevTimeoutEpilogue);
       if (!__all_sync(0xffffffffu, got)) break;
@@ -268,12 +274,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       acc_phase ^= 1;
       if (valid <= 0) continue;
-      auto lo16 = [&](uint32_t w) {
-        return fp16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xFFFF))) : __uint_as_float(w << 16);
-      };
-      auto hi16 = [&](uint32_t w) {
-        return fp16 ? __half2float(__ushort_as_half((unsigned short)(w >> 16))) : __uint_as_float(w & 0xFFFF0000u);
-      };
       // r[0..1]: gate columns nw .. + 63, r[2..3]: the other factor's.  Each
       // 32-column half is one block of the next product's K.
       const int local = t.mt * 2 * BM + slab + lane;      // row within the group
@@ -284,14 +284,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t bytes = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        if (p.bias != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 bg = *reinterpret_cast<const float4*>(bias_tab + 32 * i + j),
+                         bu = *reinterpret_cast<const float4*>(bias_tab + 64 + 32 * i + j);
+            const float g4[4] = {bg.x, bg.y, bg.z, bg.w}, u4[4] = {bu.x, bu.y, bu.z, bu.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              r[i][j + x] = __float_as_uint(__fadd_rn(__uint_as_float(r[i][j + x]), g4[x]));
+              r[2 + i][j + x] = __float_as_uint(__fadd_rn(__uint_as_float(r[2 + i][j + x]), u4[x]));
+            }
+          }
+        }
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const uint32_t bg = __shfl_sync(0xffffffffu, bias4.x, 16 * i + j / 2),
-                         bu = __shfl_sync(0xffffffffu, bias4.y, 16 * i + j / 2);
-          const float hv = mx_swiglu(__fadd_rn(__uint_as_float(r[i][j]), j & 1 ? hi16(bg) : lo16(bg)),
-                                     __fadd_rn(__uint_as_float(r[2 + i][j]), j & 1 ? hi16(bu) : lo16(bu)));
-          r[i][j] = __float_as_uint(hv);
+          r[i][j] = __float_as_uint(mx_swiglu(__uint_as_float(r[i][j]), __uint_as_float(r[2 + i][j])));
           top = max(top, r[i][j] & 0x7FFFFFFFu);
         }
         const uint32_t sb = mx_scale_byte(top);
