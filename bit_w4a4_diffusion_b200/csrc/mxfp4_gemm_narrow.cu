@@ -28,10 +28,10 @@
 // 15.7 us, 4.6 TB/s (one CTA per SM with a ring of 200 KB: 17.3).
 //
 // With a handful of rows the quantizer runs inside (kX): one more warp per
-// stage reads x, a K slice at a time, and writes the codes and scale bytes of the row
-// operand straight into the stage, in the layout TMA would have left.  Every
-// tile repeats that work, which is little for few rows, and the layer is one
-// launch instead of two.
+// stage reads x, a K slice at a time, and writes the codes and scale bytes of
+// the row operand straight into the stage, in the layout TMA would have left.
+// Every tile repeats that work, which is little for few rows, and the layer is
+// one launch instead of two.
 //
 // Roles (6 warps): 0-3 epilogue (tensor-memory lane quarter = warp), 4 TMA
 // producer, 5 MMA issuer; kX: 6 on, quantizer.  Role loops run on whole warps
@@ -78,7 +78,9 @@ struct Cfg {
 
 static_assert(kMxFusedRows <= 32, "a warp's lanes hold the row index");
 template <bool kGlu, int kX>
-constexpr int num_threads() { return (QUANT_WARP + (kX == kNoX ? 0 : Cfg<kGlu>::kStages)) * 32; }   // a quantizer warp per stage
+constexpr int num_threads() {           // a quantizer warp per stage
+  return (QUANT_WARP + (kX == kNoX ? 0 : Cfg<kGlu>::kStages)) * 32;
+}
 
 struct Ctl {
   uint64_t full[4];
@@ -88,6 +90,7 @@ struct Ctl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  int filled[4];    // kX: how often each quantizer warp filled its stage
   MxSched sched;
 };
 
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
 
   if (warp == PRODUCER_WARP) {
     // -------------------------------------------------------------- producer
-    int stage = 0, e = 0;
+    int stage = 0, e = 0, issued = 0;
     uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
     bool ok = true, act_ready = !p.weights_early;
     const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
@@ -241,6 +244,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
           issue_act(stage, t, kb, boxes);
         }
         __syncwarp();
+        ++issued;
         issued_mask |= 1u << stage;
         issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
         if (++stage == C::kStages) {
@@ -250,12 +254,20 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
       }
     }
     if (!act_ready) pdl_wait();
-    // Never leave with copies in flight into shared memory.
+    // Never leave with copies in flight into shared memory.  A quantizer warp
+    // whose wait gave up owes its stage's barrier an arrival, without which
+    // the copies' phase would not end: it is made up for here, once the
+    // quantizer has come to its own end.
+    if constexpr (kFused) named_bar_sync(4, (1 + C::kStages) * 32);
     volatile int never = 0;
     const WaitCtx drain_ctx{&never, p.dev_status, kDrainLimitNs};
     for (int s = 0; s < C::kStages; ++s)
-      if (issued_mask & (1u << s))
+      if (issued_mask & (1u << s)) {
+        if (kFused && lane == 0 && ctl->filled[s] < (issued + C::kStages - 1 - s) / C::kStages)
+          mbar_arrive(smem_u32(&ctl->full[s]));
+        __syncwarp();
         mbar_wait(smem_u32(&ctl->full[s]), (issued_phase >> s) & 1, drain_ctx, kDevTimeoutDrain);
+      }
   } else if (warp == MMA_WARP) {
     // -------------------------------------------------------------- MMA issuer
     int stage = 0, e = 0, seq = 0;
@@ -360,6 +372,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
       // The whole row index (at most 32 rows), loaded at the kernel's start.
       const int index = row_index;
       int count = 0, e = 0;    // slices of all tiles so far
+      int filled = 0;
       bool ok = true;
       for (int tile = t_first; tile < num_tiles && ok; tile += t_step) {
         const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
@@ -402,11 +415,11 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
           fence_proxy_async_smem();   // the tensor core reads through the async proxy
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl->full[stage]));
+          ++filled;
         }
       }
-      // After a wait that gave up: complete the stage's barrier, on which the
-      // producer waits for its own copies.
-      if (!ok && lane == 0) mbar_arrive(smem_u32(&ctl->full[stage]));
+      if (lane == 0) ctl->filled[stage] = filled;
+      named_bar_sync(4, (1 + C::kStages) * 32);
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -623,7 +636,8 @@ cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, int num_sms
   const long long m_tiles = p.groups == 0 ? by_rows : std::min<long long>(p.rows, p.rows / ROWS + groups);
   const long long tiles = m_tiles * ((p.N + BW - 1) / BW);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.splits > 1 ? tiles * p.splits : std::min<long long>(tiles, (long long)kMxNarrowPerSm * num_sms)));
+  cfg.gridDim = dim3((unsigned)(p.splits > 1 ? tiles * p.splits
+                                             : std::min<long long>(tiles, (long long)kMxNarrowPerSm * num_sms)));
   cfg.blockDim = dim3(num_threads<kGlu, kX>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

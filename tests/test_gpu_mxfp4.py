@@ -827,6 +827,30 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         B.mxfp4_quantize(x, out=(torch.empty(40, 128, dtype=torch.uint8, device="cuda"),
                                  torch.empty(8, dtype=torch.uint8, device="cuda")))
+def test_many_waits_that_give_up_with_the_quantizer_inside():
+    """Wherever in the ring the waits give up, the kernel ends in order, with
+    its copies landed, and the next calls are right."""
+    M, N, K = 3, 40008, 8192
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = C.rows(np.random.default_rng(M), M, K, torch.bfloat16).cuda()
+    w = {"codes": torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=g),
+         "scales": torch.randint(110, 118, (B.mxfp4_scale_bytes(N, K),), dtype=torch.uint8, device="cuda",
+                                 generator=g), "N": N, "K": K}
+    want = steps_linear(x, w)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for i in range(200):
+        old = B.get_timeout_ns()
+        try:
+            B.set_timeout_ns(1 + 40 * i)
+            B.mxfp4_linear(x, w, dev_status=status)
+        finally:
+            B.set_timeout_ns(old)
+        if i % 20 == 19:
+            status.zero_()
+            same_bits(B.mxfp4_linear(x, w, dev_status=status), want)
+            assert int(status) == 0
+
+
     with pytest.raises(ValueError):
         B.mxfp4_grouped_mlp_swiglu(x, off, up, down, up_bias=torch.empty(4, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(TypeError):
