@@ -123,7 +123,9 @@ struct MxElems<kMxFp32> {
   using Raw = MxRaw32;
   static constexpr int kSize = 4;
   static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
-  static SVDQ_DEV Raw load(const uint8_t* x, bool reused) { return {mx_load_vec(x, reused), mx_load_vec(x + 16, reused)}; }
+  static SVDQ_DEV Raw load(const uint8_t* x, bool reused) {
+    return {mx_load_vec(x, reused), mx_load_vec(x + 16, reused)};
+  }
   static SVDQ_DEV uint32_t top(const Raw& r) {
     const uint32_t m = 0x7FFFFFFFu;
     return max(max(max(r.a.x & m, r.a.y & m), max(r.a.z & m, r.a.w & m)),
@@ -147,6 +149,9 @@ struct MxElems<kMxFp32> {
 SVDQ_DEV size_t mx_tile_offset(int block, int k_chunks, int chunk) {
   return ((size_t)block * k_chunks + chunk) * 512;
 }
+
+// A row's four bytes in each tile of its block.
+SVDQ_DEV int mx_row_offset(int r) { return (r & 31) * 16 + (r >> 5) * 4; }
 
 // Row groups: group e owns rows [offsets[e], offsets[e + 1]).  Its scale
 // blocks begin at block offsets[e] / 128 + e: since
@@ -244,17 +249,6 @@ SVDQ_DEV MxTile mx_decode_tile(const MxSched* s, int groups, int tile, int tiles
   t.mt = local - t.nt * mts;
   t.row0 = s->off[e] + t.mt * tile_rows;
   t.rows = min(s->off[e + 1] - t.row0, tile_rows);
-  return t;
-}
-
-// The same with a group's rows dealt out evenly, in multiples of 128, over as
-// many tiles as tile_rows makes of them.
-SVDQ_DEV MxTile mx_decode_tile_even(const MxSched* s, int groups, int tile, int tiles_n, int tile_rows, int& e) {
-  MxTile t = mx_decode_tile(s, groups, tile, tiles_n, tile_rows, e);
-  const int first = s->off[e], count = s->off[e + 1] - first, mts = s->pre[e + 1] - s->pre[e];
-  const int each = ((count + mts - 1) / mts + 127) & ~127;
-  t.row0 = first + t.mt * each;
-  t.rows = min(count - t.mt * each, each);
   return t;
 }
 

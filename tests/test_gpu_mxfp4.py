@@ -168,6 +168,20 @@ def test_bad_offsets_are_reported(monkeypatch, kernel, off):
 
 # ----------------------------------------------------------------- product --
 
+@pytest.mark.parametrize("off", [[0, 200, 100, 300], [0, 100, 301, 300], [-1, 0, 10, 300]] +
+                         [[0] * 400 + [300, 20, 300]])
+def test_bad_offsets_are_reported_by_the_quantizer_alone(off):
+    """Also where no row's group has them, and behind the first 32."""
+    x = torch.ones(300, 64, dtype=torch.bfloat16, device="cuda")
+    offs = cuda(off, torch.int32)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    codes, scales = B.mxfp4_quantize(x, offsets=offs, dev_status=status)
+    assert int(status) == 5
+    status.zero_()
+    B.mxfp4_dequantize(codes, scales, offsets=offs, dev_status=status)
+    assert int(status) == 5
+
+
 def dense_case(M, N, K, dtype, with_bias, seed, device="cuda"):
     rng = np.random.default_rng(seed)
     a, sa = C.operand(rng, M, K, -3)
