@@ -538,12 +538,17 @@ def _mx_elsewhere(index, stream):
     return torch.cuda.stream(stream)
 
 
+_MX_INT = 2**31 - 1   # the library's sizes are ints; a larger one must not reach it cut off
+
+
 def _mx_rows(t, name, dtypes):
     """(mxfp4 dtype, device index, rows, columns, row stride) of a CUDA matrix
     whose rows are contiguous; ``dtypes`` maps the accepted torch types."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != 2 or t.get_device() < 0:
         raise TypeError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
     rows, cols = t.shape
+    if rows > _MX_INT or cols > _MX_INT:
+        raise SvdqError(2, f"{name}: {rows} x {cols} is too large")
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
@@ -555,6 +560,8 @@ def _mx_codes(codes):
             codes.get_device() < 0):
         raise TypeError("codes must be a 2-D CUDA uint8 tensor")
     rows, half = codes.shape
+    if rows > _MX_INT or 2 * half > _MX_INT:
+        raise SvdqError(2, f"codes: {rows} x {2 * half} is too large")
     return codes.get_device(), rows, 2 * half
 
 
@@ -571,7 +578,7 @@ def _mx_like(t, name, index, dtype, count):
 
 def _mx_weight(w, name, index, N, K, matrices):
     """Addresses of a weight's codes and scales."""
-    if w["N"] != N or w["K"] != K or w.get("E", 1) != matrices:
+    if w["N"] != N or w["K"] != K or w.get("E", 1) != matrices or N > _MX_INT:
         raise SvdqError(2, f"{name} is {w.get('E', 1)} x [{w['N']}, {w['K']}], not {matrices} x [{N}, {K}]")
     codes, scales = w["codes"], w["scales"]
     if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or codes.get_device() != index or
@@ -591,6 +598,8 @@ def _mx_index(row_index, x_rows, index):
     if not isinstance(row_index, torch.Tensor):
         raise TypeError("row_index must be an int32 tensor")
     rows = row_index.numel()
+    if rows > _MX_INT:
+        raise SvdqError(2, f"row_index: {rows} rows are too many")
     return rows, _mx_like(row_index, "row_index", index, torch.int32, rows)
 
 

@@ -42,8 +42,8 @@ int check_rows(int rows, int K, int groups) {
     return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "K=%d must be a positive multiple of 32", K);
   if (groups < 0 || groups > kMxMaxGroups)
     return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "groups=%d must lie in [0, %d]", groups, kMxMaxGroups);
-  // Scale rows of 256 bytes are addressed with 32 bits.
-  if (scale_bytes(scale_blocks(groups, rows), K) / 256 > std::numeric_limits<int>::max())
+  // Scale rows of 256 bytes are addressed with 32 bits, up to a block past the last.
+  if (scale_bytes(scale_blocks(groups, rows) + 1, K) / 256 > std::numeric_limits<int>::max())
     return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "rows=%d K=%d groups=%d: too many scales", rows, K, groups);
   return SVDQ_OK;
 }
@@ -65,8 +65,8 @@ int check_matrix(const void* p, long long ld, int cols, int size, const char* wh
   if (!p) return record_error(SVDQ_ERR_INVALID_ARG, "null pointer argument (%s)", what);
   if (!aligned(p, 16)) return record_error(SVDQ_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
   if (ld < cols || ld * size % 16 != 0 || ld > (1ll << 40))
-    return record_error(SVDQ_ERR_INVALID_ARG, "%s: row stride %lld must be at least %d and a multiple of 16 bytes", what,
-                        ld, cols);
+    return record_error(SVDQ_ERR_INVALID_ARG, "%s: row stride %lld must be at least %d and a multiple of 16 bytes",
+                        what, ld, cols);
   return SVDQ_OK;
 }
 
@@ -82,9 +82,10 @@ int check_product(int dtype, int rows, int N, int K, int groups, long long matri
   if (int s = check_rows(rows, K, groups)) return s;
   if (N <= 0 || N % 8 != 0)
     return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "N=%d must be a positive multiple of 8", N);
-  // Weight rows and their scale rows are addressed with 32 bits.
-  const long long blocks = matrices * (((long long)N + 127) / 128);
-  if (matrices * N > std::numeric_limits<int>::max() ||
+  // Weight rows and their scale rows are addressed with 32 bits, up to a tile
+  // (three blocks) past the last.
+  const long long blocks = matrices * (((long long)N + 127) / 128) + 3;
+  if (matrices * N + 384 > std::numeric_limits<int>::max() ||
       scale_bytes(blocks, K) / 256 > std::numeric_limits<int>::max())
     return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "%lld weights of %d x %d are too many", matrices, N, K);
   const long long m_tiles = (long long)rows / 64 + (groups == 0 ? 1 : groups);

@@ -64,7 +64,8 @@ extern "C" {
 
 int mxfp4_pack_weights(int matrices, int N, int K, const uint16_t* W, uint8_t* codes, uint8_t* scales) {
   if (!shape_ok(matrices, N, K))
-    return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "matrices=%d N=%d K=%d: positive, K a multiple of 32", matrices, N, K);
+    return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "matrices=%d N=%d K=%d: positive, K a multiple of 32",
+                        matrices, N, K);
   if (!W || !codes || !scales) return record_error(SVDQ_ERR_INVALID_ARG, "null pointer argument");
   const size_t per = (size_t)mxfp4_scale_bytes(N, K);
   std::memset(scales, 0, per * matrices);
@@ -96,7 +97,8 @@ int mxfp4_pack_weights(int matrices, int N, int K, const uint16_t* W, uint8_t* c
 
 int mxfp4_scales_to_rowmajor(int matrices, int rows, int K, const uint8_t* tiled, uint8_t* rowmajor) {
   if (!shape_ok(matrices, rows, K))
-    return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "matrices=%d rows=%d K=%d: positive, K a multiple of 32", matrices, rows, K);
+    return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "matrices=%d rows=%d K=%d: positive, K a multiple of 32",
+                        matrices, rows, K);
   if (!tiled || !rowmajor) return record_error(SVDQ_ERR_INVALID_ARG, "null pointer argument");
   const size_t per = (size_t)mxfp4_scale_bytes(rows, K);
   for (long long r = 0; r < (long long)matrices * rows; ++r)
@@ -107,7 +109,8 @@ int mxfp4_scales_to_rowmajor(int matrices, int rows, int K, const uint8_t* tiled
 
 int mxfp4_scales_from_rowmajor(int matrices, int rows, int K, const uint8_t* rowmajor, uint8_t* tiled) {
   if (!shape_ok(matrices, rows, K))
-    return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "matrices=%d rows=%d K=%d: positive, K a multiple of 32", matrices, rows, K);
+    return record_error(SVDQ_ERR_UNSUPPORTED_SHAPE, "matrices=%d rows=%d K=%d: positive, K a multiple of 32",
+                        matrices, rows, K);
   if (!tiled || !rowmajor) return record_error(SVDQ_ERR_INVALID_ARG, "null pointer argument");
   const size_t per = (size_t)mxfp4_scale_bytes(rows, K);
   std::memset(tiled, 0, per * matrices);

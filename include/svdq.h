@@ -430,7 +430,7 @@ int awq_w4a16_linear(int M, int N, int K, const void* x, const void* qweight, co
  * Offsets that decrease or leave [0, rows], and row indices outside
  * [0, x_rows), are reported as code 5 through dev_status / svdq_device_status;
  * the products of such a call write nothing, a row with a bad index becomes
- * NaN.
+ * NaN.  Outputs and workspace must not overlap an input or each other.
  *
  * All entry points: K % 32 == 0, N % 8 == 0, rows from 0 (nothing is done)
  * to 2^30, groups 1 to 512.  dtype is the type of x, y and bias; the row
@@ -465,8 +465,8 @@ int mxfp4_scales_from_rowmajor(int matrices, int rows, int K, const uint8_t* row
  * gather of tokens to their experts.  With groups > 0 and offsets the scales
  * are in the grouped layout (rows outside every group are skipped);
  * groups == 0, offsets == NULL: one matrix.
- * mxfp4_dequantize: the values (bf16 or fp32, both exact) of codes and
- * scales. */
+ * mxfp4_dequantize: the values (bf16 or fp32, both exact; infinite past the
+ * type's largest) of codes and scales. */
 int mxfp4_quantize(int dtype, int rows, int K, const void* x, long long ldx, const int* row_index, int x_rows,
                    int groups, const int* offsets, void* codes, void* scales, int* dev_status, void* stream);
 int mxfp4_dequantize(int dtype, int rows, int K, const void* codes, const void* scales, int groups,

@@ -5,6 +5,8 @@ sums are exact in fp32 (mxfp4_cases.py), so y has to equal the rounded exact
 sum bit for bit, whatever the order; products of ordinary values are held to
 the bound of fp32 summation.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -166,8 +168,6 @@ def test_bad_offsets_are_reported(monkeypatch, kernel, off):
     assert (y == 7.0).all()
 
 
-# ----------------------------------------------------------------- product --
-
 @pytest.mark.parametrize("off", [[0, 200, 100, 300], [0, 100, 301, 300], [-1, 0, 10, 300]] +
                          [[0] * 400 + [300, 20, 300]])
 def test_bad_offsets_are_reported_by_the_quantizer_alone(off):
@@ -181,6 +181,8 @@ def test_bad_offsets_are_reported_by_the_quantizer_alone(off):
     B.mxfp4_dequantize(codes, scales, offsets=offs, dev_status=status)
     assert int(status) == 5
 
+
+# ----------------------------------------------------------------- product --
 
 def dense_case(M, N, K, dtype, with_bias, seed, device="cuda"):
     rng = np.random.default_rng(seed)
@@ -717,6 +719,30 @@ def test_two_streams_at_once():
             same_bits(y, want[i])
 
 
+def test_two_host_threads_at_once():
+    """Each with its stream, its layer and sizes that take different kernels."""
+    sets = [layer_set(1, T=12), layer_set(2, T=900, E=3)]
+    want = [B.mxfp4_grouped_mlp_swiglu(*s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got[i].append(B.mxfp4_grouped_mlp_swiglu(*sets[i]))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 50
+        for y in got[i]:
+            same_bits(y, want[i])
+
+
 def test_stream_argument():
     x, off, up, down = layer_set(5)
     st = torch.cuda.Stream()
@@ -801,6 +827,30 @@ def test_a_wait_that_gives_up_is_reported(monkeypatch, kernel, M, N, K):
     assert int(status) == 0
 
 
+def test_many_waits_that_give_up_with_the_quantizer_inside():
+    """Wherever in the ring the waits give up, the kernel ends in order, with
+    its copies landed, and the next calls are right."""
+    M, N, K = 3, 40008, 8192
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = C.rows(np.random.default_rng(M), M, K, torch.bfloat16).cuda()
+    w = {"codes": torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=g),
+         "scales": torch.randint(110, 118, (B.mxfp4_scale_bytes(N, K),), dtype=torch.uint8, device="cuda",
+                                 generator=g), "N": N, "K": K}
+    want = steps_linear(x, w)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for i in range(200):
+        old = B.get_timeout_ns()
+        try:
+            B.set_timeout_ns(1 + 40 * i)
+            B.mxfp4_linear(x, w, dev_status=status)
+        finally:
+            B.set_timeout_ns(old)
+        if i % 20 == 19:
+            status.zero_()
+            same_bits(B.mxfp4_linear(x, w, dev_status=status), want)
+            assert int(status) == 0
+
+
 @pytest.mark.parametrize("kernel,T", [("pair", 3000), ("narrow", 3000), (None, 12)])
 def test_a_wait_that_gives_up_in_the_mlp_is_reported(monkeypatch, kernel, T):
     pick(monkeypatch, kernel)
@@ -841,31 +891,32 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         B.mxfp4_quantize(x, out=(torch.empty(40, 128, dtype=torch.uint8, device="cuda"),
                                  torch.empty(8, dtype=torch.uint8, device="cuda")))
-def test_many_waits_that_give_up_with_the_quantizer_inside():
-    """Wherever in the ring the waits give up, the kernel ends in order, with
-    its copies landed, and the next calls are right."""
-    M, N, K = 3, 40008, 8192
-    g = torch.Generator(device="cuda").manual_seed(M)
-    x = C.rows(np.random.default_rng(M), M, K, torch.bfloat16).cuda()
-    w = {"codes": torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=g),
-         "scales": torch.randint(110, 118, (B.mxfp4_scale_bytes(N, K),), dtype=torch.uint8, device="cuda",
-                                 generator=g), "N": N, "K": K}
-    want = steps_linear(x, w)
-    status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    for i in range(200):
-        old = B.get_timeout_ns()
-        try:
-            B.set_timeout_ns(1 + 40 * i)
-            B.mxfp4_linear(x, w, dev_status=status)
-        finally:
-            B.set_timeout_ns(old)
-        if i % 20 == 19:
-            status.zero_()
-            same_bits(B.mxfp4_linear(x, w, dev_status=status), want)
-            assert int(status) == 0
-
-
     with pytest.raises(ValueError):
         B.mxfp4_grouped_mlp_swiglu(x, off, up, down, up_bias=torch.empty(4, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(TypeError):
         B.mxfp4_linear(x[:, :128].contiguous(), w1, bias=torch.empty(256, dtype=torch.float16, device="cuda"))
+
+
+def test_sizes_past_an_int_are_refused():
+    """They would reach the library cut off (views of one element, no memory)."""
+    huge = 2**32 + 32
+    x, off, up, _ = layer_set(4)
+    with pytest.raises(B.SvdqError):
+        B.mxfp4_quantize(x[:1, :1].expand(huge, 1))
+    with pytest.raises(B.SvdqError):
+        B.mxfp4_quantize(x[:1, :1].expand(1, huge))
+    with pytest.raises(B.SvdqError):
+        B.mxfp4_quantize(x, row_index=off[:1].expand(huge))
+    with pytest.raises(B.SvdqError):
+        B.mxfp4_dequantize(up["codes"].reshape(-1)[:1].expand(huge, 1), up["scales"])
+    with pytest.raises(B.SvdqError):
+        B.mxfp4_linear(x, {**up, "E": 1, "N": huge})
+
+
+def test_values_past_the_largest_become_infinite():
+    """Scale bytes that the quantizer never writes: 6 * 2^127 and so on."""
+    a = np.full((1, 32), 7, np.uint8)      # codes of 6
+    for byte, want in ((252, 6.0 * 2.0**125), (253, np.inf), (254, np.inf)):
+        scales = cuda(O.tile(np.full((1, 1), byte, np.uint8), 32))
+        v = B.mxfp4_dequantize(cuda(O.pack(a)), scales, dtype=torch.float32).cpu()
+        assert (v == want).all(), byte
