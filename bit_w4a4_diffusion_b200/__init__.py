@@ -1,9 +1,10 @@
 """B200 (sm_100a) SVDQuant W4A4 and AWQ W4A16 linear layers.
 
-Thin ctypes binding over ``lib/libsvdq_b200.so`` (C ABI in ``include/svdq.h``).
-Every function here only marshals arguments: it checks dtypes / devices,
-allocates outputs with torch when the caller gives none, and passes raw
-pointers and the current CUDA stream to the library.  All arithmetic of the
+Thin ctypes binding over ``lib/libsvdq_b200.so`` (C ABI in ``include/svdq.h``);
+the MXFP4 calls, whose kernels are short, go through the extension module
+``_mxfp4``, which does the same.  Every function here only marshals arguments:
+it checks dtypes / devices, allocates outputs with torch when the caller gives
+none, and passes raw pointers and the current CUDA stream to the library.  All arithmetic of the
 layer happens in the library's CUDA kernels (or, for the offline weight pack,
 in its C++ host code).  If the library is missing, importing this package
 raises: there is no fallback.
@@ -89,6 +90,10 @@ def _load():
 
 
 lib = _load()
+
+from . import _mxfp4  # noqa: E402  (linked to the library that _load checks for)
+
+_mxfp4.set_error(SvdqError)
 
 
 def _check(status):
@@ -445,7 +450,6 @@ def awq_w4a16_linear(x, w, bias=None, y=None, stream=None):
 
 # ------------------------------------------------------------------ MXFP4
 
-MXFP4_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MXFP4_MAX_GROUPS = 512
 MXFP4_FUSED_ROWS = 4
 MXFP4_FUSED_GROUPED_ROWS = 16
@@ -454,7 +458,7 @@ MXFP4_FUSED_GROUPED_ROWS = 16
 def mxfp4_scale_bytes(rows, K, groups=0):
     """Bytes of the tiled E8M0 scales of [rows, K]; with ``groups`` those of
     the grouped layout.  -1 for unsupported arguments, as in the library
-    (computed here: every call needs it)."""
+    (computed here, where sizes past an int are not cut off)."""
     if rows < 0 or K <= 0 or K % 32 or not 0 <= groups <= MXFP4_MAX_GROUPS:
         return -1
     return (rows // 128 + groups if groups else (rows + 127) // 128) * ((K + 127) // 128) * 512
@@ -517,139 +521,16 @@ def mxfp4_scales_from_rowmajor(rowmajor):
     return out
 
 
-def _raw_stream(index):
-    return torch.cuda.current_stream(index).cuda_stream
-
-
-# The same handle without a Stream object (3 us of a call's 10), where this
-# torch has it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
-
-
-def _mx_elsewhere(index, stream):
-    """The context in which a call on another device or stream than the
-    current ones is made: what it allocates then belongs to that stream."""
-    if stream is None:
-        return torch.cuda.device(index)
+def _mx_elsewhere(t, stream):
+    """The context in which a call on another stream than the current one is
+    made: what it allocates then belongs to that stream."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("a CUDA tensor is expected")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=index)
-    if stream.device_index != index:
-        raise ValueError(f"the stream is of device {stream.device_index}, the tensors of device {index}")
+        stream = torch.cuda.ExternalStream(_stream(stream), device=t.device)
+    if stream.device != t.device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors of {t.device}")
     return torch.cuda.stream(stream)
-
-
-_MX_INT = 2**31 - 1   # the library's sizes are ints; a larger one must not reach it cut off
-
-
-def _mx_rows(t, name, dtypes):
-    """(mxfp4 dtype, device index, rows, columns, row stride) of a CUDA matrix
-    whose rows are contiguous; ``dtypes`` maps the accepted torch types."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != 2 or t.get_device() < 0:
-        raise TypeError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    rows, cols = t.shape
-    if rows > _MX_INT or cols > _MX_INT:
-        raise SvdqError(2, f"{name}: {rows} x {cols} is too large")
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return dtypes[t.dtype], t.get_device(), rows, cols, ld if rows > 1 else cols
-
-
-def _mx_codes(codes):
-    if (not isinstance(codes, torch.Tensor) or codes.dtype is not torch.uint8 or codes.dim() != 2 or
-            codes.get_device() < 0):
-        raise TypeError("codes must be a 2-D CUDA uint8 tensor")
-    rows, half = codes.shape
-    if rows > _MX_INT or 2 * half > _MX_INT:
-        raise SvdqError(2, f"codes: {rows} x {2 * half} is too large")
-    return codes.get_device(), rows, 2 * half
-
-
-def _mx_like(t, name, index, dtype, count):
-    """Data pointer of a contiguous tensor of ``count`` elements, or of None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
-        raise TypeError(f"{name} must be a {dtype} tensor on cuda:{index}")
-    if t.numel() != count or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and have {count} elements (it has {t.numel()})")
-    return t.data_ptr()
-
-
-def _mx_weight(w, name, index, N, K, matrices):
-    """Addresses of a weight's codes and scales."""
-    if w["N"] != N or w["K"] != K or w.get("E", 1) != matrices or N > _MX_INT:
-        raise SvdqError(2, f"{name} is {w.get('E', 1)} x [{w['N']}, {w['K']}], not {matrices} x [{N}, {K}]")
-    codes, scales = w["codes"], w["scales"]
-    if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or codes.get_device() != index or
-            scales.get_device() != index):
-        raise TypeError(f"{name}: codes and scales must be uint8 tensors on cuda:{index}")
-    tiles = matrices * ((N + 127) // 128) * ((K + 127) // 128)
-    if (codes.numel() != matrices * N * (K // 2) or scales.numel() != 512 * tiles or not codes.is_contiguous() or
-            not scales.is_contiguous()):
-        raise ValueError(f"{name}: codes and scales must be contiguous and those of {matrices} x [{N}, {K}]")
-    return codes.data_ptr(), scales.data_ptr()
-
-
-def _mx_index(row_index, x_rows, index):
-    """(rows, address) of a row index, or of none: row i is row i of x."""
-    if row_index is None:
-        return x_rows, None
-    if not isinstance(row_index, torch.Tensor):
-        raise TypeError("row_index must be an int32 tensor")
-    rows = row_index.numel()
-    if rows > _MX_INT:
-        raise SvdqError(2, f"row_index: {rows} rows are too many")
-    return rows, _mx_like(row_index, "row_index", index, torch.int32, rows)
-
-
-def _mx_groups(offsets, index):
-    """(groups, address of the offsets)."""
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
-        raise TypeError("offsets must be an int32 tensor [groups + 1]")
-    n = offsets.numel()
-    return n - 1, _mx_like(offsets, "offsets", index, torch.int32, n)
-
-
-def _mx_out(y, rows, N, dtype, device):
-    """(y, its row stride): the caller's, checked, or a new one."""
-    if y is None:
-        return torch.empty_strided((rows, N), (N, 1), dtype=dtype, device=device), N
-    _, _, y_rows, y_cols, ldy = _mx_rows(y, "y", {dtype: 0})
-    if y_rows != rows or y_cols != N or y.device != device:
-        raise ValueError(f"y must be [{rows}, {N}] on {device}")
-    return y, ldy
-
-
-def _mx_quantized(out, rows, K, size, device):
-    """Codes [rows, K/2] and scales (``size`` bytes): the caller's pair,
-    checked, or new; and their addresses."""
-    if out is None:
-        codes = torch.empty_strided((rows, K // 2), (K // 2, 1), dtype=torch.uint8, device=device)
-        scales = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=device)
-        return codes, scales, codes.data_ptr(), scales.data_ptr()
-    codes, scales = out
-    return (codes, scales, _mx_like(codes, "codes", device.index, torch.uint8, rows * (K // 2)),
-            _mx_like(scales, "scales", device.index, torch.uint8, size))
-
-
-def _mx_workspace(workspace, need, device):
-    """(tensor to keep until the launch, pointer, bytes)."""
-    if need < 0:
-        raise SvdqError(2, "unsupported shape")
-    if workspace is None:
-        if need == 0:
-            return None, None, 0
-        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
-        return workspace, workspace.data_ptr(), need
-    if workspace.dtype is not torch.uint8 or workspace.device != device or not workspace.is_contiguous():
-        raise TypeError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return workspace, workspace.data_ptr(), workspace.numel()
-
-
-_MX_INPUT = MXFP4_DTYPES
-_MX_LAYER = {torch.bfloat16: 0, torch.float16: 1}
-_MX_VALUES = {torch.bfloat16: 0, torch.float32: 2}
 
 
 def mxfp4_quantize(x, offsets=None, row_index=None, out=None, dev_status=None, stream=None):
@@ -657,47 +538,20 @@ def mxfp4_quantize(x, offsets=None, row_index=None, out=None, dev_status=None, s
     tiled E8M0 scales uint8).  ``row_index`` (int32 [rows]): row i is
     x[row_index[i]].  ``offsets`` (int32 [groups + 1]): scales in the grouped
     layout; rows of no group are skipped."""
-    dtype, index, x_rows, K, ldx = _mx_rows(x, "x", _MX_INPUT)
-    if stream is not None or index != torch.cuda.current_device():
-        with _mx_elsewhere(index, stream):
-            return mxfp4_quantize(x, offsets, row_index, out, dev_status)
-    rows, idx = _mx_index(row_index, x_rows, index)
-    groups, off = (0, None) if offsets is None else _mx_groups(offsets, index)
-    size = mxfp4_scale_bytes(rows, K, groups)
-    if size < 0:
-        raise SvdqError(2, f"unsupported shape rows={rows} K={K} groups={groups}")
-    codes, scales, codes_ptr, scales_ptr = _mx_quantized(out, rows, K, size, x.device)
-    status = lib.mxfp4_quantize(dtype, rows, K, x.data_ptr(), ldx, idx, x_rows, groups, off, codes_ptr, scales_ptr,
-                                _mx_like(dev_status, "dev_status", index, torch.int32, 1), _raw_stream(index))
-    if status:
-        _check(status)
-    return codes, scales
+    if stream is None:
+        return _mxfp4.quantize(x, offsets, row_index, out, dev_status)
+    with _mx_elsewhere(x, stream):
+        return _mxfp4.quantize(x, offsets, row_index, out, dev_status)
 
 
 def mxfp4_dequantize(codes, scales, offsets=None, dtype=torch.bfloat16, out=None, dev_status=None, stream=None):
     """The values (bf16 or fp32 [rows, K]) that codes and scales stand for;
     with ``offsets`` rows of no group are left as they were (0 in a new
     output)."""
-    index, rows, K = _mx_codes(codes)
-    if stream is not None or index != torch.cuda.current_device():
-        with _mx_elsewhere(index, stream):
-            return mxfp4_dequantize(codes, scales, offsets, dtype, out, dev_status)
-    if dtype not in _MX_VALUES:
-        raise TypeError("dtype must be torch.bfloat16 or torch.float32")
-    groups, off = (0, None) if offsets is None else _mx_groups(offsets, index)
-    size = mxfp4_scale_bytes(rows, K, groups)
-    if size < 0:
-        raise SvdqError(2, f"unsupported shape rows={rows} K={K} groups={groups}")
-    if out is None and offsets is not None:
-        out = torch.zeros((rows, K), dtype=dtype, device=codes.device)
-    out, ldo = _mx_out(out, rows, K, dtype, codes.device)
-    status = lib.mxfp4_dequantize(_MX_VALUES[dtype], rows, K,
-                                  _mx_like(codes, "codes", index, torch.uint8, rows * (K // 2)),
-                                  _mx_like(scales, "scales", index, torch.uint8, size), groups, off, out.data_ptr(),
-                                  ldo, _mx_like(dev_status, "dev_status", index, torch.int32, 1), _raw_stream(index))
-    if status:
-        _check(status)
-    return out
+    if stream is None:
+        return _mxfp4.dequantize(codes, scales, offsets, dtype, out, dev_status)
+    with _mx_elsewhere(codes, stream):
+        return _mxfp4.dequantize(codes, scales, offsets, dtype, out, dev_status)
 
 
 def mxfp4_gemm(codes, scales, w, bias=None, dtype=torch.bfloat16, y=None, dev_status=None, stream=None):
@@ -712,66 +566,28 @@ def mxfp4_grouped_gemm(codes, scales, offsets, w, bias=None, dtype=torch.bfloat1
     """mxfp4_gemm per row group: rows offsets[e] .. offsets[e + 1] - 1 with
     weight e ("E" matrices).  Rows of no group are left as they were (not
     initialized in a new output)."""
-    index, rows, K = _mx_codes(codes)
-    if stream is not None or index != torch.cuda.current_device():
-        with _mx_elsewhere(index, stream):
-            return mxfp4_grouped_gemm(codes, scales, offsets, w, bias, dtype, y, dev_status)
-    if dtype not in _MX_LAYER:
-        raise TypeError("dtype must be torch.bfloat16 or torch.float16")
-    N = w["N"]
-    groups, off = (0, None) if offsets is None else _mx_groups(offsets, index)
-    wc, ws = _mx_weight(w, "w", index, N, K, groups or 1)
-    y, ldy = _mx_out(y, rows, N, dtype, codes.device)
-    status = lib.mxfp4_grouped_gemm(_MX_LAYER[dtype], groups, rows, N, K, off,
-                                    _mx_like(codes, "codes", index, torch.uint8, rows * (K // 2)),
-                                    _mx_like(scales, "scales", index, torch.uint8, mxfp4_scale_bytes(rows, K, groups)),
-                                    wc, ws, _mx_like(bias, "bias", index, dtype, (groups or 1) * N), y.data_ptr(),
-                                    ldy, _mx_like(dev_status, "dev_status", index, torch.int32, 1),
-                                    _raw_stream(index))
-    if status:
-        _check(status)
-    return y
+    if stream is None:
+        return _mxfp4.grouped_gemm(codes, scales, offsets, w, bias, dtype, y, dev_status)
+    with _mx_elsewhere(codes, stream):
+        return _mxfp4.grouped_gemm(codes, scales, offsets, w, bias, dtype, y, dev_status)
 
 
 def mxfp4_linear(x, w, bias=None, y=None, workspace=None, dev_status=None, stream=None):
     """y = Q(x) deq(W)^T + bias for x bf16 or fp16 [M, K]; y has x's type."""
-    dtype, index, M, K, ldx = _mx_rows(x, "x", _MX_LAYER)
-    if stream is not None or index != torch.cuda.current_device():
-        with _mx_elsewhere(index, stream):
-            return mxfp4_linear(x, w, bias, y, workspace, dev_status)
-    N = w["N"]
-    wc, ws = _mx_weight(w, "w", index, N, K, 1)
-    y, ldy = _mx_out(y, M, N, x.dtype, x.device)
-    workspace, ws_ptr, ws_size = _mx_workspace(workspace, mxfp4_workspace_bytes(M, K), x.device)
-    status = lib.mxfp4_linear(dtype, M, N, K, x.data_ptr(), ldx, wc, ws, _mx_like(bias, "bias", index, x.dtype, N),
-                              y.data_ptr(), ldy, ws_ptr, ws_size,
-                              _mx_like(dev_status, "dev_status", index, torch.int32, 1), _raw_stream(index))
-    if status:
-        _check(status)
-    return y
+    if stream is None:
+        return _mxfp4.linear(x, w, bias, y, workspace, dev_status)
+    with _mx_elsewhere(x, stream):
+        return _mxfp4.linear(x, w, bias, y, workspace, dev_status)
 
 
 def mxfp4_grouped_linear(x, offsets, w, row_index=None, bias=None, y=None, workspace=None, dev_status=None,
                          stream=None):
     """mxfp4_linear per row group: row i of y [rows, N] is row i of x, or
     x[row_index[i]], times the weight of the group that owns row i."""
-    dtype, index, x_rows, K, ldx = _mx_rows(x, "x", _MX_LAYER)
-    if stream is not None or index != torch.cuda.current_device():
-        with _mx_elsewhere(index, stream):
-            return mxfp4_grouped_linear(x, offsets, w, row_index, bias, y, workspace, dev_status)
-    rows, idx = _mx_index(row_index, x_rows, index)
-    N = w["N"]
-    groups, off = _mx_groups(offsets, index)
-    wc, ws = _mx_weight(w, "w", index, N, K, groups)
-    y, ldy = _mx_out(y, rows, N, x.dtype, x.device)
-    workspace, ws_ptr, ws_size = _mx_workspace(workspace, mxfp4_workspace_bytes(rows, K, groups), x.device)
-    status = lib.mxfp4_grouped_linear(dtype, groups, rows, N, K, x.data_ptr(), ldx, idx, x_rows, off, wc, ws,
-                                      _mx_like(bias, "bias", index, x.dtype, groups * N), y.data_ptr(), ldy, ws_ptr,
-                                      ws_size, _mx_like(dev_status, "dev_status", index, torch.int32, 1),
-                                      _raw_stream(index))
-    if status:
-        _check(status)
-    return y
+    if stream is None:
+        return _mxfp4.grouped_linear(x, offsets, w, row_index, bias, y, workspace, dev_status)
+    with _mx_elsewhere(x, stream):
+        return _mxfp4.grouped_linear(x, offsets, w, row_index, bias, y, workspace, dev_status)
 
 
 def mxfp4_grouped_gemm_swiglu_quant(codes, scales, offsets, w, bias=None, dtype=torch.bfloat16, out=None,
@@ -780,28 +596,10 @@ def mxfp4_grouped_gemm_swiglu_quant(codes, scales, offsets, w, bias=None, dtype=
     epilogue: w holds two matrices [I, K] per group (gate, other), bias
     [groups, 2, I] of ``dtype``.  Returns (codes [rows, I/2], grouped scales)
     of h = g sigmoid(g) u."""
-    index, rows, K = _mx_codes(codes)
-    if stream is not None or index != torch.cuda.current_device():
-        with _mx_elsewhere(index, stream):
-            return mxfp4_grouped_gemm_swiglu_quant(codes, scales, offsets, w, bias, dtype, out, dev_status)
-    if dtype not in _MX_LAYER:
-        raise TypeError("dtype must be torch.bfloat16 or torch.float16")
-    width = w["N"]
-    groups, off = _mx_groups(offsets, index)
-    wc, ws = _mx_weight(w, "w", index, width, K, 2 * groups)
-    size = mxfp4_scale_bytes(rows, width, groups)
-    if size < 0:
-        raise SvdqError(2, f"unsupported shape rows={rows} I={width} groups={groups}")
-    h_codes, h_scales, hc, hs = _mx_quantized(out, rows, width, size, codes.device)
-    status = lib.mxfp4_grouped_gemm_swiglu_quant(
-        _MX_LAYER[dtype], groups, rows, width, K, off,
-        _mx_like(codes, "codes", index, torch.uint8, rows * (K // 2)),
-        _mx_like(scales, "scales", index, torch.uint8, mxfp4_scale_bytes(rows, K, groups)), wc, ws,
-        _mx_like(bias, "bias", index, dtype, 2 * groups * width), hc, hs,
-        _mx_like(dev_status, "dev_status", index, torch.int32, 1), _raw_stream(index))
-    if status:
-        _check(status)
-    return h_codes, h_scales
+    if stream is None:
+        return _mxfp4.grouped_gemm_swiglu_quant(codes, scales, offsets, w, bias, dtype, out, dev_status)
+    with _mx_elsewhere(codes, stream):
+        return _mxfp4.grouped_gemm_swiglu_quant(codes, scales, offsets, w, bias, dtype, out, dev_status)
 
 
 def mxfp4_grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index=None, up_bias=None, down_bias=None, y=None,
@@ -809,24 +607,9 @@ def mxfp4_grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index=None, up_bias=N
     """The experts' MLP y = down(SwiGLU(up(x))) per row group: w_up two
     matrices [I, K] per group (gate, other), w_down [groups, K, I]; the hidden
     rows are quantized in the up product's epilogue."""
-    dtype, index, x_rows, K, ldx = _mx_rows(x, "x", _MX_LAYER)
-    if stream is not None or index != torch.cuda.current_device():
-        with _mx_elsewhere(index, stream):
-            return mxfp4_grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index, up_bias, down_bias, y, workspace,
-                                            dev_status)
-    rows, idx = _mx_index(row_index, x_rows, index)
-    width = w_up["N"]
-    groups, off = _mx_groups(offsets, index)
-    uc, us = _mx_weight(w_up, "w_up", index, width, K, 2 * groups)
-    dc, ds = _mx_weight(w_down, "w_down", index, K, width, groups)
-    y, ldy = _mx_out(y, rows, K, x.dtype, x.device)
-    workspace, ws_ptr, ws_size = _mx_workspace(workspace, mxfp4_mlp_workspace_bytes(groups, rows, K, width), x.device)
-    status = lib.mxfp4_grouped_mlp_swiglu(dtype, groups, rows, K, width, x.data_ptr(), ldx, idx, x_rows, off, uc, us,
-                                          _mx_like(up_bias, "up_bias", index, x.dtype, 2 * groups * width), dc, ds,
-                                          _mx_like(down_bias, "down_bias", index, x.dtype, groups * K), y.data_ptr(),
-                                          ldy, ws_ptr, ws_size,
-                                          _mx_like(dev_status, "dev_status", index, torch.int32, 1),
-                                          _raw_stream(index))
-    if status:
-        _check(status)
-    return y
+    if stream is None:
+        return _mxfp4.grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index, up_bias, down_bias, y, workspace,
+                                         dev_status)
+    with _mx_elsewhere(x, stream):
+        return _mxfp4.grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index, up_bias, down_bias, y, workspace,
+                                         dev_status)

@@ -1,13 +1,16 @@
-"""Build the CUDA library ``libsvdq_b200.so`` in-tree with nvcc (sm_100a).
+"""Build the CUDA library ``libsvdq_b200.so`` in-tree with nvcc (sm_100a), and
+the module through which Python calls its MXFP4 part.
 
 Usage: ``python bit_w4a4_diffusion_b200/build.py [-v]`` (or ``build()`` from
 ``__graft_entry__``); run it by path -- importing the package loads the
 library this script produces.  Objects are rebuilt only when a source or header is
 newer than the object.  Cross-compiles without a GPU.
 """
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "lib", "libsvdq_b200.so")
+BIND = os.path.join(PKG, "_mxfp4.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -27,6 +31,7 @@ CU_SOURCES = ["abi.cu", "quantize_act.cu", "quantize_nvfp4.cu", "gemm_nvfp4.cu",
               "mxfp4_abi.cu", "mxfp4_quant.cu", "mxfp4_gemm_pair.cu",
               "mxfp4_gemm_pair_swiglu.cu", "mxfp4_gemm_narrow.cu"]
 CXX_SOURCES = ["pack.cpp", "calib.cpp", "mxfp4_pack.cpp"]
+BIND_SOURCE = "mxfp4_bind.cpp"
 
 
 def _headers():
@@ -74,7 +79,22 @@ def build(verbose=False, ptxas_verbose=False):
             _run(["g++"] + CXX_FLAGS + ["-c", s, "-o", o], verbose)
     if _stale(LIB, objs):
         _run([NVCC] + ARCH + ["-shared", "-o", LIB] + objs + ["-lpthread"], verbose)
+    _build_bind(hdrs, verbose)
     return LIB
+
+
+def _build_bind(hdrs, verbose):
+    """The extension module, against the installed torch and the library."""
+    src = os.path.join(CSRC, BIND_SOURCE)
+    if not _stale(BIND, [src] + hdrs):
+        return
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+             "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+             "-I", "/usr/local/cuda/include"]
+    libs = ["-L", os.path.dirname(LIB), "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"), "-ltorch_python",
+            "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN/lib"]
+    _run(["g++"] + flags + [src, "-o", BIND] + libs, verbose)
 
 
 if __name__ == "__main__":

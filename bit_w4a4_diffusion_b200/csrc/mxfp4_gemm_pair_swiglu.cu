@@ -8,9 +8,9 @@
 // What bounds it: the operands' way from L2 to shared memory, about 84 GB/s
 // per SM with every SM loading; a 256-column K slice of a tile is 35 KB per SM
 // (rows 16 KB, 128 weight rows 16 KB, scales 3 KB) for 256 x 256 x 256
-// multiply-adds on two SMs.  The rows are the M operand here (in
-// mxfp4_gemm_pair.cu the weight is): a thread then holds a row's gate and
-// other values side by side, and whole blocks of 32 hidden columns.
+// multiply-adds on two SMs.  The rows are the M operand, so that a thread
+// holds a row's gate and other values side by side, and whole blocks of 32
+// hidden columns.
 //
 // A cluster of two CTAs computes a tile: CTA r holds rows [128 r, + 128) of
 // the tile, CTA 0 the gate's weight rows and CTA 1 the other factor's, the
