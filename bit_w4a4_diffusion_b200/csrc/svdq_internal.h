@@ -341,13 +341,20 @@ struct MxPerDevice {
     return cudaSuccess;
   }
 };
-// Opts a kernel into `bytes` of dynamic shared memory, once per device.
+// Opts a kernel into `bytes` of dynamic shared memory, once per device, and
+// asks for the largest split of shared memory: an SM cannot take CTAs of a
+// kernel with another split before it has drained, which kept a short kernel
+// from starting beside the one before it (quantize and dequantize of 1001 x
+// 4096, 9.0 us with the default, 6.0 with this).
 template <auto kKernel>
 cudaError_t mx_allow_smem(int bytes) {
   static MxPerDevice<int> done;
   int got = 0;
   return done.get(&got, [&](int* n) {
     *n = bytes;
+    if (cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared))
+      return e;
     return cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   });
 }
