@@ -167,9 +167,9 @@ struct MxSched {
   int pre[kMxMaxGroups + 1];
 };
 
-// Filled by one whole warp; all loads go out before the first is used.
-// Offsets that decrease or leave [0, rows] give an empty schedule and a status
-// code.
+// Filled by one whole warp.  Offsets that decrease or leave [0, rows] give an
+// empty schedule and a status code.  (Short code on purpose: it runs once, and
+// instructions that are not in the cache yet take longer than they run.)
 SVDQ_DEV void mx_build_sched(MxSched* s, int groups, const int* offsets, int rows, int tile_rows, int* dev_status) {
   const int lane = threadIdx.x & 31;
   if (groups == 0) {
@@ -181,24 +181,17 @@ SVDQ_DEV void mx_build_sched(MxSched* s, int groups, const int* offsets, int row
     }
     return;
   }
-  constexpr int kRounds = kMxMaxGroups / 32 + 1;   // groups + 1 offsets, 32 at a time
-  int off[kRounds];
-#pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    const int e = 32 * i + lane;
-    off[i] = e <= groups ? __ldg(offsets + e) : 0;
-  }
+#pragma unroll 4
+  for (int e = lane; e <= groups; e += 32) s->off[e] = __ldg(offsets + e);
+  __syncwarp();
   int run = 0;
   bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    if (32 * i > groups) break;
-    const int e = 32 * i + lane, lo = off[i];
-    int hi = __shfl_down_sync(0xffffffffu, lo, 1);
-    const int next = i + 1 < kRounds ? __shfl_sync(0xffffffffu, off[i + 1 < kRounds ? i + 1 : i], 0) : 0;
-    if (lane == 31) hi = next;
+#pragma unroll 1
+  for (int base = 0; base < groups; base += 32) {
+    const int e = base + lane;
     int t = 0;
     if (e < groups) {
+      const int lo = s->off[e], hi = s->off[e + 1];
       const bool wrong = lo < 0 || hi < lo || hi > rows;
       bad |= wrong;
       t = wrong ? 0 : (hi - lo + tile_rows - 1) / tile_rows;
@@ -208,10 +201,7 @@ SVDQ_DEV void mx_build_sched(MxSched* s, int groups, const int* offsets, int row
       const int o = __shfl_up_sync(0xffffffffu, t, d);
       if (lane >= d) t += o;
     }
-    if (e <= groups) {
-      s->off[e] = lo;
-      if (e < groups) s->pre[e + 1] = run + t;
-    }
+    if (e < groups) s->pre[e + 1] = run + t;
     run += __shfl_sync(0xffffffffu, t, 31);
   }
   if (lane == 0) s->pre[0] = 0;
@@ -245,7 +235,7 @@ SVDQ_DEV MxTile mx_decode_tile(const MxSched* s, int groups, int tile, int tiles
   const int local = tile - first * tiles_n, mts = s->pre[e + 1] - first;
   MxTile t;
   t.e = e;
-  t.nt = local / mts;
+  t.nt = mts == 1 ? local : local / mts;
   t.mt = local - t.nt * mts;
   t.row0 = s->off[e] + t.mt * tile_rows;
   t.rows = min(s->off[e + 1] - t.row0, tile_rows);

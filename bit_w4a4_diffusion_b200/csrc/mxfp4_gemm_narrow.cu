@@ -58,28 +58,31 @@ constexpr unsigned long long kDrainLimitNs = 2000000000ull;
 // other's loads, and a dependent kernel finds room before this one ends.
 constexpr int TMEM_COLS = 256;
 constexpr int ROWS = kMxNarrowRows;     // rows per tile (MMA N)
-template <bool kGlu>
+template <bool kGlu, int kX>
 struct Cfg {
   static constexpr int kWeights = kGlu ? 2 : 1;                   // weight tiles, and accumulators, per tile
-  static constexpr int kStages = kGlu ? 2 : 3;
+  static constexpr int kRows = kX == kNoX ? ROWS : kMxFusedRows;  // rows that a stage has room for
+  static constexpr int kChunk = kRows < 32 ? kRows : 32;          // rows of one step of the epilogue
+  static constexpr int kStages = kGlu ? 2 : kX == kNoX ? 3 : 4;
   static constexpr int kBufs = kGlu ? 1 : 2;                      // accumulator buffers
-  static constexpr int kActBytes = ROWS * BK_BYTES;
+  static constexpr int kActBytes = kRows * BK_BYTES;
   static constexpr int kSfOff = kWeights * W_BYTES + kActBytes;   // SFW (per weight), then SFA
   static constexpr int kStageBytes = kSfOff + (kWeights + 1) * SF_BYTES;
-  static constexpr int kAccCols = kWeights * ROWS;                // per accumulator buffer
+  static constexpr int kAccRows = kRows < 32 ? 32 : kRows;        // columns of an accumulator, read 32 at a time
+  static constexpr int kAccCols = kWeights * kAccRows;            // per accumulator buffer
   static constexpr int kSfCols = 8 * kWeights + 8;
   static constexpr int kTmemSf = kBufs * kAccCols;
-  // Output staging: two buffers of 32 rows x 128 columns, or (SwiGLU) per
-  // epilogue warp 32 rows x 32 hidden columns of fp32, rows 36 words apart.
-  static constexpr int kStageOutBytes = kGlu ? EPI_WARPS * 32 * H_PITCH * 4 : 2 * 32 * BW * 2;
+  // Output staging: two buffers of a step's rows x 128 columns, or (SwiGLU) per
+  // epilogue warp its rows x 32 hidden columns of fp32, rows 36 words apart.
+  static constexpr int kStageOutBytes = kGlu ? EPI_WARPS * kChunk * H_PITCH * 4 : 2 * kChunk * BW * 2;
   static_assert(kStageBytes % 1024 == 0, "stages keep the 1024-byte alignment of SWIZZLE_128B");
   static_assert(kTmemSf + kStages * kSfCols <= TMEM_COLS, "accumulators and scale buffers fit tensor memory");
 };
 
-static_assert(kMxFusedRows <= 32, "a warp's lanes hold the row index");
+static_assert(kMxFusedRows == 16, "an MMA's least N; a warp's lanes hold the row index");
 template <bool kGlu, int kX>
 constexpr int num_threads() {           // a quantizer warp per stage
-  return (QUANT_WARP + (kX == kNoX ? 0 : Cfg<kGlu>::kStages)) * 32;
+  return (QUANT_WARP + (kX == kNoX ? 0 : Cfg<kGlu, kX>::kStages)) * 32;
 }
 
 struct Ctl {
@@ -94,17 +97,20 @@ struct Ctl {
   MxSched sched;
 };
 
-template <bool kGlu>
-constexpr size_t smem_bytes() {
-  return 1024 + Cfg<kGlu>::kStages * Cfg<kGlu>::kStageBytes + Cfg<kGlu>::kStageOutBytes + sizeof(Ctl);
+template <bool kGlu, int kX>
+constexpr int smem_bytes() {
+  using C = Cfg<kGlu, kX>;
+  return 1024 + C::kStages * C::kStageBytes + C::kStageOutBytes + (int)sizeof(Ctl);
 }
-// 228 KB per SM, 1 KB of it reserved for each CTA.
-static_assert(kMxNarrowPerSm * (smem_bytes<false>() + 1024) <= 233472 &&
-                  kMxNarrowPerSm * (smem_bytes<true>() + 1024) <= 233472,
+template <bool kGlu, int kX>
+constexpr bool fits() {
+  using C = Cfg<kGlu, kX>;
+  // 228 KB per SM, 1 KB of it reserved for each CTA; partial sums reuse the ring.
+  return kMxNarrowPerSm * (smem_bytes<kGlu, kX>() + 1024) <= 233472 &&
+         C::kRows * C::kWeights * BW * 4 <= C::kStages * C::kStageBytes;
+}
+static_assert(fits<false, kNoX>() && fits<true, kNoX>() && fits<false, kMxBf16>() && fits<true, kMxBf16>(),
               "two CTAs fit an SM");
-static_assert(ROWS * BW * 4 <= Cfg<false>::kStages * Cfg<false>::kStageBytes &&
-                  ROWS * 2 * BW * 4 <= Cfg<true>::kStages * Cfg<true>::kStageBytes,
-              "partial sums reuse the ring");
 
 SVDQ_DEV float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     mxfp4_gemm_narrow_kernel(const __grid_constant__ CUtensorMap tm_act, const __grid_constant__ CUtensorMap tm_w,
                              const __grid_constant__ CUtensorMap tm_sfa, const __grid_constant__ CUtensorMap tm_sfw,
                              const MxGemmParams p) {
-  using C = Cfg<kGlu>;
+  using C = Cfg<kGlu, kX>;
   constexpr bool kFused = kX != kNoX;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -153,35 +159,46 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     tmem_alloc(smem_u32(&ctl->tmem_base), TMEM_COLS);
     tmem_relinquish();
   }
+  // Scalars of the whole kernel, before the wait: its end is the start of the
+  // path that a layer with few rows is made of.
+  const int groups = p.groups == 0 ? 1 : p.groups;
+  const int k_slices = (p.K + 255) / 256, k_chunks = (p.K + 127) / 128;
+  const int tiles_n = (p.N + BW - 1) / BW;
+  const int splits = p.splits, split_bits = __ffs(splits) - 1;   // a power of two
+  const uint32_t rank = splits > 1 ? cluster_ctarank() : 0;
+  // This CTA's part of K (whole K without splits) and its tiles.
+  int kb_begin = k_slices * (int)rank >> split_bits;
+  int kb_end = k_slices * ((int)rank + 1) >> split_bits;
+  int t_first = (int)blockIdx.x >> split_bits, t_step = (int)gridDim.x >> split_bits;
+  const MxSched* const sched = &ctl->sched;
+  const WaitCtx wctx{&ctl->abort_flag, p.dev_status, p.timeout_ns};
+
   // Offsets are an input like the weights: with weights_early both were
-  // complete before the preceding kernel began.
-  if (!p.weights_early) pdl_wait();
+  // complete before the preceding kernel began.  Without groups there are none.
+  const bool sched_waits = !p.weights_early && p.groups != 0;
+  if (sched_waits) pdl_wait();
   int row_index = 0;
-  if (kFused && warp >= QUANT_WARP && p.row_index != nullptr && lane < p.rows) row_index = __ldg(p.row_index + lane);
+  if (kFused && sched_waits && warp >= QUANT_WARP && p.row_index != nullptr && lane < p.rows)
+    row_index = __ldg(p.row_index + lane);
   if (warp == 0) mx_build_sched(&ctl->sched, p.groups, p.offsets, p.rows, ROWS, p.dev_status);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
+  uint32_t tmem = ctl->tmem_base;
+  int num_tiles = sched->pre[groups] * tiles_n;
+  int e0 = 0;
+  MxTile first = {};
+  if (t_first < num_tiles) first = mx_decode_tile(sched, groups, t_first, tiles_n, ROWS, e0);
+  // Computed here, not behind the wait.
+  asm volatile("" : "+r"(kb_begin), "+r"(kb_end), "+r"(t_first), "+r"(t_step), "+r"(num_tiles), "+r"(tmem));
+  asm volatile("" : "+r"(first.e), "+r"(first.nt), "+r"(first.mt), "+r"(first.row0), "+r"(first.rows));
+  if (!p.weights_early && !sched_waits) pdl_wait();
   pdl_launch_dependents();
-
-  const MxSched* const sched = &ctl->sched;
-  const int groups = p.groups == 0 ? 1 : p.groups;
-  const int k_slices = (p.K + 255) / 256, k_chunks = (p.K + 127) / 128;
-  const int tiles_n = (p.N + BW - 1) / BW;
-  const int num_tiles = sched->pre[groups] * tiles_n;
-  const int splits = p.splits;
-  const uint32_t rank = splits > 1 ? cluster_ctarank() : 0;
-  // This CTA's part of K (whole K without splits) and its tiles.
-  const int kb_begin = (int)((long long)k_slices * (int)rank / splits);
-  const int kb_end = (int)((long long)k_slices * ((int)rank + 1) / splits);
-  const int t_first = (int)blockIdx.x / splits, t_step = (int)gridDim.x / splits;
-  const WaitCtx wctx{&ctl->abort_flag, p.dev_status, p.timeout_ns};
 
   if (warp == PRODUCER_WARP) {
     // -------------------------------------------------------------- producer
-    int stage = 0, e = 0, issued = 0;
+    int stage = 0, e = e0, issued = 0;
     uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
     bool ok = true, act_ready = !p.weights_early;
     const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
@@ -210,7 +227,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
                        pol_a);
     };
     for (int tile = t_first; tile < num_tiles && ok; tile += t_step) {
-      const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
+      const MxTile t = tile == t_first ? first : mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
       const int boxes = (t.rows + kMxNarrowBox - 1) / kMxNarrowBox;
       int kb = kb_begin;
       if (!act_ready) {
@@ -270,11 +287,11 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
       }
   } else if (warp == MMA_WARP) {
     // -------------------------------------------------------------- MMA issuer
-    int stage = 0, e = 0, seq = 0;
+    int stage = 0, e = e0, seq = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int tile = t_first; tile < num_tiles && ok; tile += t_step, ++seq) {
-      const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
+      const MxTile t = tile == t_first ? first : mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
       const int a = seq % C::kBufs;
       if (!mbar_wait_warp(smem_u32(&ctl->acc_empty[a]), ((seq / C::kBufs) & 1) ^ 1, wctx, kDevTimeoutMma)) break;
       tc_fence_after();
@@ -309,7 +326,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
             if (s < steps) {
 #pragma unroll
               for (int i = 0; i < C::kWeights; ++i)
-                mma_mxfp4(tmem + a * C::kAccCols + i * ROWS, mx_operand_desc(base + i * W_BYTES + 32 * s),
+                mma_mxfp4(tmem + a * C::kAccCols + i * C::kAccRows, mx_operand_desc(base + i * W_BYTES + 32 * s),
                           mx_operand_desc(sb + 32 * s), s & 1 ? idesc1 : idesc0, sf + 8 * i + 4 * (s >> 1),
                           sf + 8 * C::kWeights + 4 * (s >> 1) + sfa_off, kb > kb_begin || s > 0 ? 1u : 0u);
             }
@@ -371,11 +388,11 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
       using Raw = typename E::Raw;
       // The whole row index (at most 32 rows), loaded at the kernel's start.
       const int index = row_index;
-      int count = 0, e = 0;    // slices of all tiles so far
+      int count = 0, e = e0;   // slices of all tiles so far
       int filled = 0;
       bool ok = true;
       for (int tile = t_first; tile < num_tiles && ok; tile += t_step) {
-        const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
+        const MxTile t = tile == t_first ? first : mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
         for (int kb = kb_begin; kb < kb_end && ok; ++kb, ++count) {
           if (count % C::kStages != stage) continue;
           const uint32_t phase = (uint32_t)(count / C::kStages) & 1;
@@ -426,9 +443,9 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     // Thread = weight row (output column); a tensor-memory column = a row of y.
     const int q = warp;
     const bool fp16 = p.fp16 != 0;
-    int e = 0, seq = 0, out_seq = 0;
+    int e = e0, seq = 0, out_seq = 0;
     for (int tile = t_first; tile < num_tiles; tile += t_step, ++seq) {
-      const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
+      const MxTile t = tile == t_first ? first : mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
       const int a = seq % C::kBufs;
       const int n0 = t.nt * BW, n = n0 + 32 * q + lane;
       float b0 = 0.f, b1 = 0.f;
@@ -446,7 +463,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
         tmem_ld_32x32b_x32(acc + 32 * c, r);
         if constexpr (kGlu) {
           uint32_t r2[32];
-          tmem_ld_32x32b_x32(acc + ROWS + 32 * c, r2);
+          tmem_ld_32x32b_x32(acc + C::kAccRows + 32 * c, r2);
           tmem_ld_wait(r);
           reg_fence(r2);
           if (c == chunks - 1) {
@@ -458,7 +475,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
             // Partial sums, [row][gate 128 | other 128] fp32 in the drained ring.
             float* part = reinterpret_cast<float*>(smem) + 32 * c * 2 * BW + 32 * q + lane;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < C::kChunk; ++j) {
               part[j * 2 * BW] = __uint_as_float(r[j]);
               part[j * 2 * BW + BW] = __uint_as_float(r2[j]);
             }
@@ -473,10 +490,10 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
           uint8_t* const codes = p.h_codes + (size_t)(t.row0 + 32 * c) * (p.N / 2) + (n0 + 32 * q) / 2;
           // h goes through shared memory, so that a lane then holds a row's
           // whole block: its maximum, scale and codes need no other lane.
-          float* const hbuf = reinterpret_cast<float*>(out_base) + q * 32 * H_PITCH;
+          float* const hbuf = reinterpret_cast<float*>(out_base) + q * C::kChunk * H_PITCH;
           __syncwarp();   // the reads of the chunk before are done
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < C::kChunk; ++j)
             hbuf[j * H_PITCH + lane] =
                 mx_swiglu(__fadd_rn(__uint_as_float(r[j]), b0), __fadd_rn(__uint_as_float(r2[j]), b1));
           __syncwarp();
@@ -515,14 +532,14 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
             // Partial sums, [row][128 weight rows] fp32 in the drained ring.
             float* part = reinterpret_cast<float*>(smem) + 32 * c * BW + 32 * q + lane;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) part[j * BW] = __uint_as_float(r[j]);
+            for (int j = 0; j < C::kChunk; ++j) part[j * BW] = __uint_as_float(r[j]);
             continue;
           }
-          uint8_t* const buf = out_base + (out_seq & 1) * (32 * BW * 2);
+          uint8_t* const buf = out_base + (out_seq & 1) * (C::kChunk * BW * 2);
           ++out_seq;
           uint16_t* const col = reinterpret_cast<uint16_t*>(buf) + 32 * q + lane;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
+          for (int j = 0; j < C::kChunk; j += 2) {
             const uint32_t w = mx_pack16(__fadd_rn(__uint_as_float(r[j]), b0),
                                          __fadd_rn(__uint_as_float(r[j + 1]), b0), fp16);
             col[j * BW] = (uint16_t)w;
@@ -532,7 +549,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
           // other, which every thread reaches after its reads of the first.
           named_bar_sync(3, EPI_WARPS * 32);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < C::kChunk / 8; ++i) {
             const int v = threadIdx.x + 128 * i, j = v >> 4, x = v & 15;
             if (32 * c + j < t.rows && n0 + 8 * x < p.N)
               *reinterpret_cast<uint4*>(p.y + (size_t)(t.row0 + 32 * c + j) * p.ldy + n0 + 8 * x) =
@@ -550,8 +567,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     // four columns a lane.
     cluster_sync();
     if (t_first < num_tiles) {
-      int e = 0;
-      const MxTile t = mx_decode_tile(sched, groups, t_first, tiles_n, ROWS, e);
+      const MxTile t = first;
       const bool fp16 = p.fp16 != 0;
       const int n = t.nt * BW + 4 * lane;
       const bool in_n = n < p.N;          // N is a multiple of 8 (SwiGLU: 32)
@@ -626,9 +642,9 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
 
 template <bool kGlu, int kX>
 cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, int num_sms, cudaStream_t stream, bool pdl) {
-  using C = Cfg<kGlu>;
+  using C = Cfg<kGlu, kX>;
   auto kernel = mxfp4_gemm_narrow_kernel<kGlu, kX>;
-  constexpr int smem = (int)smem_bytes<kGlu>();
+  constexpr int smem = smem_bytes<kGlu, kX>();
   if (cudaError_t e = mx_allow_smem<mxfp4_gemm_narrow_kernel<kGlu, kX>>(smem)) return e;
   // As many tiles as the rows can make: every group's last tile may be short.
   const long long groups = p.groups == 0 ? 1 : p.groups;
