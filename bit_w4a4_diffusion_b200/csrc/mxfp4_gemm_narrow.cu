@@ -112,6 +112,11 @@ constexpr bool fits() {
 static_assert(fits<false, kNoX>() && fits<true, kNoX>() && fits<false, kMxBf16>() && fits<true, kMxBf16>(),
               "two CTAs fit an SM");
 
+// A cluster barrier that orders nothing: the loads before it have returned,
+// and the stores to y need not have (with release semantics it waits for them).
+SVDQ_DEV void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 SVDQ_DEV float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
         }
       }
     }
-    cluster_sync();   // no CTA leaves while its partial sums are being read
+    cluster_meet();   // no CTA leaves while its partial sums are being read
   }
   tc_fence_before();
   __syncthreads();
