@@ -100,8 +100,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc_pair(smem_u32(&ctl->tmem_base), TMEM_COLS);
     tmem_relinquish_pair();
   }
-  pdl_wait();                // inputs of the preceding kernel's making, the offsets too
-  pdl_launch_dependents();
+  // Inputs may be of the preceding kernel's making, the offsets too; without
+  // groups all that comes before the loads goes before the wait.
+  if (p.groups != 0) pdl_wait();
   if (warp == 0) mx_build_sched(&ctl->sched, p.groups, p.offsets, p.rows, 2 * BM, p.dev_status);
   // Both CTAs' barriers and tensor memory exist before either is used.
   __syncwarp();
@@ -116,6 +117,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int tiles_n = (p.N + BN_HALF - 1) / BN_HALF;         // = the 128-row scale blocks of one weight matrix
   const int num_tiles = sched->pre[groups] * tiles_n;
   const WaitCtx wctx{&ctl->abort_flag, p.dev_status, p.timeout_ns};
+  if (p.groups == 0) pdl_wait();
+  pdl_launch_dependents();
 
   if (warp == PRODUCER_WARP) {
     // -------------------------------------------------------------- producer

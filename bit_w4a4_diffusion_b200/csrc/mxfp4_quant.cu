@@ -71,17 +71,14 @@ SVDQ_DEV Place place(int cta, int k_slices, int spread) {
 }
 
 // With groups the grid's first CTA reports offsets that decrease or leave [0,
-// rows] (the others look only at those of their own rows) and does nothing else.
-// Returns the index among the other CTAs.  On a warp that has rows as well the
-// check took 0.3 to 0.9 us.
-SVDQ_DEV int check_offsets(int rows, int groups, const int* offsets, int* dev_status) {
-  if (groups == 0) return (int)blockIdx.x;
-  if (blockIdx.x == 0 && dev_status)
-    for (int e = threadIdx.x; e < groups; e += blockDim.x) {
-      const int lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
-      if (lo < 0 || hi < lo || hi > rows) atomicCAS(dev_status, 0, kDevBadIndex);
-    }
-  return (int)blockIdx.x - 1;
+// rows] (the others look only at those of their own rows) and does nothing
+// else.  On a warp that has rows as well the check took 0.3 to 0.9 us.
+SVDQ_DEV void check_offsets(int rows, int groups, const int* offsets, int* dev_status) {
+  if (!dev_status) return;
+  for (int e = threadIdx.x; e < groups; e += blockDim.x) {
+    const int lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
+    if (lo < 0 || hi < lo || hi > rows) atomicCAS(dev_status, 0, kDevBadIndex);
+  }
 }
 
 // Where the codes and scales of one row are: its row of the matrix (-1: none,
@@ -182,11 +179,13 @@ __global__ void __launch_bounds__(quant_warps<kDtype>() * 32) mxfp4_quantize_ker
   constexpr int kWarps = quant_warps<kDtype>(), kUnit = unit_bytes<kDtype>();
   constexpr int kChunks = 32 * E::kSize / 16;           // 16-byte chunks of a block: 4 or 8
   extern __shared__ __align__(128) uint8_t staging[];
-  pdl_wait();
-  // Every CTA of this grid has begun by the time a dependent kernel starts.
-  pdl_launch_dependents();
-  const int cta = check_offsets(p.rows, p.groups, p.offsets, p.dev_status);
-  if (cta < 0) return;
+  if (kGrouped && blockIdx.x == 0) {
+    pdl_wait();
+    pdl_launch_dependents();
+    check_offsets(p.rows, p.groups, p.offsets, p.dev_status);
+    return;
+  }
+  const int cta = (int)blockIdx.x - kGrouped;
   const Place at = place<kWarps>(cta, k_slices, spread);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = at.block * 128, count = min(p.rows - row0, 128);
@@ -201,6 +200,11 @@ __global__ void __launch_bounds__(quant_warps<kDtype>() * 32) mxfp4_quantize_ker
   const uint32_t row_bytes = (uint32_t)min(p.K - k0, MQ_COLS) * E::kSize;
   const bool gather = p.row_index != nullptr;
 
+  // What needs no input comes before the wait for the preceding kernel.  A
+  // dependent kernel starts when every CTA is behind this point or has had
+  // nothing to do, and so after the preceding kernel's end.
+  pdl_wait();
+  pdl_launch_dependents();
   // Lane 4 t + i holds the place of row i of the warp's quad t, and where it
   // comes from: -1 no row, or of no group, -2 out of range.
   const RowPlace mine = lane_row<kGrouped>(at, row0, count, p.rows, p.groups, p.offsets);
@@ -290,10 +294,13 @@ __global__ void __launch_bounds__(8 * 32) mxfp4_dequantize_kernel(const MxDequan
   constexpr int kSize = kDtype == kMxFp32 ? 4 : 2;
   constexpr int kUnit = unit_bytes<kDtype>();
   extern __shared__ __align__(128) uint8_t staging[];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int cta = check_offsets(p.rows, p.groups, p.offsets, p.dev_status);
-  if (cta < 0) return;
+  if (kGrouped && blockIdx.x == 0) {
+    pdl_wait();
+    pdl_launch_dependents();
+    check_offsets(p.rows, p.groups, p.offsets, p.dev_status);
+    return;
+  }
+  const int cta = (int)blockIdx.x - kGrouped;
   const Place at = place<8>(cta, k_slices, spread);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = at.block * 128, count = min(p.rows - row0, 128);
@@ -306,8 +313,10 @@ __global__ void __launch_bounds__(8 * 32) mxfp4_dequantize_kernel(const MxDequan
   const bool g_ok = k0 + 32 * g < p.K;
   const uint8_t* const codes = p.codes + (size_t)row0 * (p.K / 2) + k0 / 2 + 16 * g;
   const int chunk = at.slice * 2 + (g >> 2);
-  const RowPlace mine = lane_row<kGrouped>(at, row0, count, p.rows, p.groups, p.offsets);
   const uint32_t row_bytes = (uint32_t)min(p.K - k0, MQ_COLS) * kSize;
+  pdl_wait();
+  pdl_launch_dependents();
+  const RowPlace mine = lane_row<kGrouped>(at, row0, count, p.rows, p.groups, p.offsets);
   uint4 w[MQ_UNITS];
   uint32_t b[MQ_UNITS];
 #pragma unroll
