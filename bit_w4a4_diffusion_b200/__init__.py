@@ -451,7 +451,7 @@ def awq_w4a16_linear(x, w, bias=None, y=None, stream=None):
 # ------------------------------------------------------------------ MXFP4
 
 MXFP4_MAX_GROUPS = 512
-MXFP4_FUSED_ROWS = 4
+MXFP4_FUSED_ROWS = 8
 MXFP4_FUSED_GROUPED_ROWS = 16
 
 

@@ -124,9 +124,10 @@ int quantize(const Device& d, int dtype, int rows, int K, const void* x, long lo
 }
 
 // Few enough rows that the narrow kernel quantizes x itself: one launch, no
-// workspace for x.  GPU time of a 4096 x 4096 layer, one kernel / two: 6.0 /
-// 6.9 us at one row, 7.4 / 7.2 at four, 8.8 / 7.2 at eight, and the second
-// launch costs the host 3 us.  Grouped rows count by the largest group, which
+// workspace for x.  GPU time, one kernel / two, us: 4096 x 4096 6.9 / 7.3 at
+// five rows, 7.0 / 7.5 at eight, 8.0 / 7.5 at twelve; 12288 x 4096 12.2 / 11.4
+// at eight, 16.6 / 11.4 at twelve; and the second launch and the workspace cost
+// the host 3 us.  Grouped rows count by the largest group, which
 // the host does not know: up to 16 rows are rarely many of one group.
 bool fuses(int groups, int rows) { return rows <= (groups == 0 ? MXFP4_FUSED_ROWS : MXFP4_FUSED_GROUPED_ROWS); }
 
@@ -147,30 +148,34 @@ bool forced(const char* name, size_t n) {
 // Which kernel a product takes, unless one is forced.  The narrow kernel while its
 // tiles fit the chip's CTA slots once, or while a group has so few rows on
 // average that the weight bytes dominate.  GPU time narrow / pair, us:
-//   dense, 4096 x 4096: M = 64 6.6 / 10.4, 512 9.9 / 11.0, 768 15.5 / 11.7;
-//   1024 x 4096: 2048 9.8 / 11.0;  12288 x 4096: 192 11.9 / 12.6, 256 17.2 / 12.9
-//   32 groups, 2048 x 2048, rows each: 96 21.9 / 22.2, 128 25.8 / 24.3
-//   SwiGLU, the same: 96 34.9 / 36.4, 128 36.7 / 36.7, 160 44.5 / 36.9
+//   dense, 4096 x 4096: M = 64 6.7 / 10.4, 512 10.3 / 11.2, 768 16.4 / 11.7;
+//   1024 x 4096: 2048 10.4 / 11.0;  12288 x 4096: 192 11.8 / 12.3, 256 17.4 / 12.4
+//   32 groups, 2048 x 2048, rows each: 96 21.0 / 22.4, 128 21.8 / 23.5, 160 27.5 / 23.9
+//   SwiGLU, the same: 64 27.0 / 33.6, 96 34.7 / 33.8, 160 43.8 / 34.3
+//   MLP, 32 uneven groups, 2048 x 1024: 75 rows 36.5 / 40.2, 125 46.5 / 42.9 (up product)
 bool use_pair(int groups, int rows, int N, bool swiglu, int sms) {
   if (forced("pair", 4)) return true;
   if (forced("narrow", 6)) return false;
   if (narrow_m_tiles(groups, rows) * ((N + 127) / 128) <= (long long)kMxNarrowPerSm * sms) return false;
-  return rows / (groups == 0 ? 1 : groups) > (swiglu ? 128 : 96);
+  return rows / (groups == 0 ? 1 : groups) > (swiglu ? 96 : 128);
 }
 
 // CTAs (a cluster) that share one tile's K: as many as there are SMs for, each
-// with at least four 256-column slices (SwiGLU, whose ring holds two: two).
-// GPU time, us, of 1, 2, 4, 8 CTAs:
-//   1 row, 4096 x 4096 (32 tiles): 8.7, 6.8, 5.9, 6.2;  64 rows: 9.8, 9.1, 7.9, 9.7
-//   77 rows, 5000 x 2080 (80 tiles): 8.0, 9.6
-//   2 experts' rows, 4096 x 4096 (64 tiles): 10.0, 8.6, 8.2, 13.0;  SwiGLU: 16.2, 12.9, 11.8, 17.2
-// Up to two CTAs per SM would take the last 5% of a single product with few
-// rows, but in the MLP they leave the next product no room to load its
-// weights ahead (8 experts, 2048 x 1024: 17.1 us against 15.8).
+// with at least four 256-column slices (SwiGLU, whose ring holds two: two), or
+// as two CTAs to an SM take, each with at least eight.  GPU time, us, of 1, 2,
+// 4, 8 CTAs:
+//   32 tiles: 1 x 4096 x 4096 8.1, 6.3, 5.6, 5.6;  64 rows 10.4, 9.3, 8.0, 9.2
+//   64 tiles: 1 x 8192 x 8192 13.6, 10.6, 9.6, 13.5;  2 experts' rows, 4096 x
+//   4096 9.3, 7.3, 7.0, 11.2;  SwiGLU 15.3, 11.9, 11.1, 15.6
+//   80 tiles: 77 x 5000 x 2080 8.5, 9.4;  77 x 5000 x 8192 16.6, 13.8, 15.7
+//   96 tiles: 8 x 12288 x 4096 12.2, 10.6, 14.0
+// With less than eight slices each, two CTAs to an SM gain nothing and leave
+// an MLP's next product no room to load its weights ahead.
 int choose_splits(long long tiles, int K, bool swiglu, int sms) {
   const int slices = (K + 255) / 256, least = swiglu ? 2 : 4;
   for (int s = 8; s > 1; s /= 2)
-    if (tiles * s <= sms && slices >= s * least) return s;
+    if ((tiles * s <= sms && slices >= s * least) || (tiles * s <= (long long)kMxNarrowPerSm * sms && slices >= s * 8))
+      return s;
   return 1;
 }
 

@@ -441,7 +441,7 @@ int awq_w4a16_linear(int M, int N, int K, const void* x, const void* qweight, co
 typedef enum { MXFP4_BF16 = 0, MXFP4_FP16 = 1, MXFP4_FP32 = 2 } mxfp4_dtype;
 #define MXFP4_MAX_GROUPS 512
 /* Up to this many rows the layers quantize x inside the product's kernel. */
-#define MXFP4_FUSED_ROWS 4
+#define MXFP4_FUSED_ROWS 8
 #define MXFP4_FUSED_GROUPED_ROWS 16
 #define SVDQ_DEV_BAD_INDEX 5 /* device status code: offsets or row_index out of range */
 

@@ -301,7 +301,7 @@ def steps_linear(x, w, bias=None, **kw):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N,K", [(8, 32), (136, 96), (1000, 544), (2056, 4096)])
 def test_linear_around_the_fused_limit(N, K, dtype):
-    """Up to four rows the product quantizes x itself: the same bits as the two
+    """Up to eight rows the product quantizes x itself: the same bits as the two
     steps, below the limit and above, special values included."""
     rng = np.random.default_rng(N + K)
     w = B.to_device(B.mxfp4_pack_weights(F.bf16_bits(rng.standard_normal((N, K)).astype(np.float32))))
@@ -310,7 +310,7 @@ def test_linear_around_the_fused_limit(N, K, dtype):
     base[3, 8] = float("inf")
     base[5, 20:K] = 0
     base[6] *= 2.0 ** -18 if dtype == torch.float16 else 2.0 ** -120
-    for M in (1, 2, 3, 4, 5, 8, 40):
+    for M in (1, 2, 3, 4, 5, 6, 7, 8, 9, 40):
         x = base[:M, 8:8 + K]
         same_bits(B.mxfp4_linear(x, w, bias=b), steps_linear(x, w, b))
 
