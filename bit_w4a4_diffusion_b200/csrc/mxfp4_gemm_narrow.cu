@@ -23,9 +23,12 @@
 // CTAs shares one tile's K range and adds its partial sums through
 // distributed shared memory, always in rank order.
 //
-// Measured (GPU time of the product): 32 groups of 32 rows, 2048 x 8192: 48.9
-// us, 5.8 TB/s of weights; SwiGLU of them 87.4 us, 6.5 TB/s; 32 x 2048 x 2048
-// 15.7 us, 4.6 TB/s (one CTA per SM with a ring of 200 KB: 17.3).
+// Measured (GPU time of the product): 32 groups of 32 rows, 2048 x 8192: 46.3
+// us, 6.2 TB/s of weights; SwiGLU of them 86.6 us, 6.6 TB/s; 32 x 2048 x 2048
+// 14.8 us, 4.8 TB/s (one CTA per SM with a ring of 200 KB took 10% more).  One
+// row, 4096 x 4096: 4.9 us, of which 1 us is the preceding kernel's end, 1.8
+// until the last weights are there, 0.5 the last MMAs and 1.5 the sum over the
+// cluster.
 //
 // With a handful of rows the quantizer runs inside (kX): one more warp per
 // stage reads x, a K slice at a time, and writes the codes and scale bytes of
