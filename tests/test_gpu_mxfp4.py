@@ -5,6 +5,8 @@ sums are exact in fp32 (mxfp4_cases.py), so y has to equal the rounded exact
 sum bit for bit, whatever the order; products of ordinary values are held to
 the bound of fp32 summation.
 """
+import collections
+import sys
 import threading
 
 import numpy as np
@@ -920,3 +922,66 @@ def test_values_past_the_largest_become_infinite():
         scales = cuda(O.tile(np.full((1, 1), byte, np.uint8), 32))
         v = B.mxfp4_dequantize(cuda(O.pack(a)), scales, dtype=torch.float32).cpu()
         assert (v == want).all(), byte
+
+
+def test_binding_arguments():
+    """Weights of any mapping; wrong ones are refused before anything runs."""
+    x, off, up, down = layer_set(4)
+    want = B.mxfp4_grouped_mlp_swiglu(x, off, up, down)
+    same_bits(B.mxfp4_grouped_mlp_swiglu(x, off, collections.UserDict(up), collections.UserDict(down)), want)
+    codes, scales = B.mxfp4_quantize(x, offsets=off)
+    with pytest.raises(KeyError):
+        B.mxfp4_grouped_mlp_swiglu(x, off, up, {k: v for k, v in down.items() if k != "scales"})
+    with pytest.raises(TypeError):
+        B.mxfp4_grouped_mlp_swiglu(x, off, up, {**down, "codes": down["codes"].cpu()})
+    with pytest.raises(TypeError):
+        B.mxfp4_grouped_mlp_swiglu(x, off, up, None)
+    with pytest.raises(TypeError):
+        B.mxfp4_grouped_linear(x, None, down)
+    with pytest.raises(TypeError):
+        B.mxfp4_grouped_gemm(codes, scales, off, down, dtype=torch.float32)
+    with pytest.raises(TypeError):
+        B.mxfp4_dequantize(codes, scales, offsets=off, dtype=torch.float16)
+    with pytest.raises(TypeError):
+        B.mxfp4_dequantize(codes, None, offsets=off)
+    with pytest.raises(TypeError):
+        B.mxfp4_quantize(x, out=codes)
+    with pytest.raises(ValueError):
+        B.mxfp4_quantize(x, out=(codes,))
+    with pytest.raises(TypeError):
+        B.mxfp4_grouped_mlp_swiglu(x, off, up, down, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(B.SvdqError) as e:
+        B.mxfp4_grouped_mlp_swiglu(x, off, up, down, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 1 and "workspace" in str(e.value)
+    with pytest.raises(ValueError):
+        B.mxfp4_quantize(x, stream=torch.cuda.Stream(), out=(codes[:, :8], scales))
+    same_bits(B.mxfp4_grouped_mlp_swiglu(x, off, up, down), want)
+
+
+def test_binding_keeps_no_references():
+    """References to arguments and results are given back, by calls that
+    succeed and by refused ones."""
+    x, off, up, down = layer_set(4)
+    y = torch.empty_like(x)
+    out = B.mxfp4_quantize(x, offsets=off)
+    objects = [x, off, y, up, down, up["codes"], up["scales"], down["codes"], down["scales"], out, *out]
+
+    def calls():
+        B.mxfp4_grouped_mlp_swiglu(x, off, up, down)
+        assert B.mxfp4_grouped_mlp_swiglu(x, off, up, down, y=y) is y
+        assert B.mxfp4_quantize(x, offsets=off, out=out)[0] is out[0]
+        B.mxfp4_dequantize(*out, offsets=off)
+        for bad in (lambda: B.mxfp4_grouped_linear(x, off, up), lambda: B.mxfp4_grouped_linear(x, off[:-1], down),
+                    lambda: B.mxfp4_quantize(x, offsets=off, out=(out[0], out[0])),
+                    lambda: B.mxfp4_grouped_mlp_swiglu(x, off, up, down, y=x[:3])):
+            with pytest.raises((B.SvdqError, ValueError)):
+                bad()
+
+    calls()
+    torch.cuda.synchronize()
+    before, held = [sys.getrefcount(o) for o in objects], torch.cuda.memory_allocated()
+    for _ in range(50):
+        calls()
+    torch.cuda.synchronize()
+    assert [sys.getrefcount(o) for o in objects] == before
+    assert torch.cuda.memory_allocated() == held
