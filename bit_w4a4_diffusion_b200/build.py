@@ -86,9 +86,9 @@ def build(verbose=False, ptxas_verbose=False):
 def _build_bind(hdrs, verbose):
     """The extension module, against the installed torch and the library."""
     src = os.path.join(CSRC, BIND_SOURCE)
-    if not _stale(BIND, [src] + hdrs):
-        return
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    if not _stale(BIND, [src, os.path.join(torch, "version.py")] + hdrs):
+        return
     flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
              "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
              "-I", "/usr/local/cuda/include"]
