@@ -312,9 +312,17 @@ SVDQ_DEV uint32_t mx_pack16(float a, float b, bool fp16) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// g sigmoid(g) u.  The exponential and the quotient are the fast intrinsics
-// (relative error below 2^-20 for the |g| that leave sigmoid away from 0 and
-// 1): the value is rounded to 4 bits next.
-SVDQ_DEV float mx_swiglu(float g, float u) { return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u); }
+// g sigmoid(g) u, with the exponential of -|g|, which never leaves the range
+// (with exp(-g) the quotient is 0 from g = -87.3 on, where the divisor passes
+// 2^126, however large u).  The exponential and the quotient are the fast
+// intrinsics (relative error below 2^-20 while exp(-|g|) is normal, its last
+// place of 2^-149 behind that): the value is rounded to 4 bits next.  Against
+// exp(-g) alone the SwiGLU pair kernel takes 110.5 us instead of 108.7 (16 x
+// 1024 rows, 2048 of 4096); no difference was found with few rows.
+SVDQ_DEV float mx_swiglu(float g, float u) {
+  const float t = __expf(-fabsf(g));
+  const float n = g < 0.0f ? __fmul_rn(g, t) : g;
+  return __fmul_rn(__fdividef(n, __fadd_rn(1.0f, t)), u);
+}
 
 }  // namespace svdq
