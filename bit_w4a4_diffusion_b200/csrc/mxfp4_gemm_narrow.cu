@@ -298,6 +298,9 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     int stage = 0, e = e0, seq = 0;
     uint32_t phase = 0;
     bool ok = true;
+    // Only the producer runs ahead of the preceding kernel: the others' bounded
+    // waits begin behind it, so that its time does not count against them.
+    if (p.weights_early) pdl_wait();
     for (int tile = t_first; tile < num_tiles && ok; tile += t_step, ++seq) {
       const MxTile t = tile == t_first ? first : mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
       const int a = seq % C::kBufs;
@@ -452,6 +455,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
     const int q = warp;
     const bool fp16 = p.fp16 != 0;
     int e = e0, seq = 0, out_seq = 0;
+    if (p.weights_early) pdl_wait();
     for (int tile = t_first; tile < num_tiles; tile += t_step, ++seq) {
       const MxTile t = tile == t_first ? first : mx_decode_tile(sched, groups, tile, tiles_n, ROWS, e);
       const int a = seq % C::kBufs;

@@ -37,7 +37,8 @@
  *    current device, else SVDQ_ERR_UNSUPPORTED_DEVICE.  There is no fallback.
  *  - Every kernel is launched with programmatic dependent launch: it may be
  *    scheduled while the previous work on the stream finishes, and waits for
- *    that work's completion before it touches global memory.  Setting the
+ *    that work's completion before it touches global memory.  (One exception,
+ *    behind kernels of the same call only: see the MXFP4 section.)  Setting the
  *    environment variable SVDQ_PDL=0 launches plainly (read at every call).
  *  - Kernel choice (environment, read at every call; results are the same
  *    either way, bit for bit up to the summation order of fp32 low-rank
@@ -437,7 +438,11 @@ int awq_w4a16_linear(int M, int N, int K, const void* x, const void* qweight, co
  * strides ldx, ldy, ldo are in elements and multiples of 16 bytes.  Matrix
  * and bias pointers are 16-byte, offsets and row_index 4-byte aligned.
  * The conventions at the top of this file hold (streams, errors, dev_status,
- * PDL). */
+ * PDL), with one exception: in a call of several kernels a product may read
+ * its weights, bias and offsets while the kernel of the same call before it
+ * still runs.  The call's first kernel has waited for all earlier work on the
+ * stream by then, so weights written just before the call are the ones used.
+ * The limit of a kernel's waits does not include that kernel's time. */
 typedef enum { MXFP4_BF16 = 0, MXFP4_FP16 = 1, MXFP4_FP32 = 2 } mxfp4_dtype;
 #define MXFP4_MAX_GROUPS 512
 /* Up to this many rows the layers quantize x inside the product's kernel. */

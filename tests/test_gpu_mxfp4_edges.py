@@ -1,5 +1,7 @@
 """MXFP4 operators on the GPU where they could go wrong unnoticed: the ends of
-the range."""
+the range, waits beside a slow kernel."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +9,7 @@ import torch
 import bit_w4a4_diffusion_b200 as B
 from oracle import formats as F
 from oracle import mxfp4 as O
+from tests import mxfp4_cases as C
 from tests.helpers import nibbles
 
 pytestmark = pytest.mark.gpu
@@ -58,3 +61,48 @@ def test_swiglu_of_gates_whose_exponential_leaves_the_range(monkeypatch, kernel,
     low, high = (F.E2M1_VALUE[O._encode64((h + d) / s)] for d in (-delta, delta))
     got = F.e2m1_decode(got_c)
     assert ((got >= low) & (got <= high)).all()
+
+
+# ------------------------------------------------------- -------------- waits --
+
+def random_weight(lead, N, K, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    E = int(np.prod(lead))
+    return {"codes": torch.randint(0, 256, (*lead, N, K // 2), dtype=torch.uint8, device="cuda", generator=g),
+            "scales": torch.randint(110, 118, (*lead, B.mxfp4_scale_bytes(N, K)), dtype=torch.uint8, device="cuda",
+                                    generator=g), "N": N, "K": K, "E": E}
+
+
+def test_waiting_for_the_kernel_before_is_no_timeout():
+    """The products of an MLP start while the kernels before them still run.
+    Here the quantizer takes long: its rows come from pinned host memory, over
+    a link that a copy keeps busy (0.3 ms).  The products must not count that
+    against the limit of their own waits, which take a few microseconds."""
+    E, rows, K, width = 2, 128, 32768, 256
+    x = C.rows(np.random.default_rng(0), rows, K, torch.bfloat16)
+    off = cuda([0, 80, rows], torch.int32)
+    up, down = random_weight((E, 2), width, K), random_weight((E,), K, width, 1)
+    want = B.mxfp4_grouped_mlp_swiglu(x.cuda(), off, up, down)
+    host = x.pin_memory()
+    y = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(B.mxfp4_mlp_workspace_bytes(E, rows, K, width), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    stream, other = torch.cuda.current_stream().cuda_stream, torch.cuda.Stream()
+    src, dst = torch.empty(1 << 29, dtype=torch.uint8, pin_memory=True), torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    old = B.get_timeout_ns()
+    try:
+        B.set_timeout_ns(4000)
+        for _ in range(3):
+            torch.cuda.synchronize()
+            with torch.cuda.stream(other):
+                dst.copy_(src, non_blocking=True)     # 10 ms
+            time.sleep(0.002)
+            assert B.lib.mxfp4_grouped_mlp_swiglu(
+                0, E, rows, K, width, host.data_ptr(), K, None, rows, off.data_ptr(), up["codes"].data_ptr(),
+                up["scales"].data_ptr(), None, down["codes"].data_ptr(), down["scales"].data_ptr(), None, y.data_ptr(),
+                K, ws.data_ptr(), ws.numel(), status.data_ptr(), stream) == 0
+            torch.cuda.synchronize()
+            assert int(status) == 0
+            assert torch.equal(y, want)
+    finally:
+        B.set_timeout_ns(old)
