@@ -322,26 +322,43 @@ constexpr int kMxFusedRows = 16;    // most rows of a product that quantizes x i
 cudaError_t launch_mxfp4_gemm_narrow(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, int num_sms,
                                      cudaStream_t stream, bool pdl);
 
-// A value found once per device (0: not yet found; the finder gives > 0).
+// Unique id (cuCtxGetId) of the calling thread's current CUDA context, or 0
+// when no context is current or the driver cannot tell.  Ids are never
+// reused within a process, so what was found under one id (a device address,
+// a kernel's attributes) is known to be stale once the id changes (for example
+// after cudaDeviceReset).
+unsigned long long current_context_id();
+
+// A value found once per device and context; like a kernel's attributes, it
+// does not hold in another context, nor after a reset.  The finder gives the
+// same value in every context of a device, so that whoever sees its own
+// context's id beside the value may use it.
 constexpr int kMxMaxDevices = 64;
 template <class T>
 struct MxPerDevice {
-  std::atomic<T> v[kMxMaxDevices] = {};
+  struct Slot {
+    std::atomic<unsigned long long> ctx_id{0};
+    std::atomic<T> v{};
+  };
+  Slot slots[kMxMaxDevices];
   template <class F>
   cudaError_t get(T* out, F&& find) {
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     if (dev < 0 || dev >= kMxMaxDevices) return cudaErrorInvalidDevice;
-    T got = v[dev].load(std::memory_order_acquire);
-    if (got == T{}) {
-      if (cudaError_t e = find(&got)) return e;
-      v[dev].store(got, std::memory_order_release);
+    const unsigned long long ctx = current_context_id();
+    Slot& s = slots[dev];
+    if (ctx == 0 || s.ctx_id.load(std::memory_order_acquire) != ctx) {
+      T found{};
+      if (cudaError_t e = find(&found)) return e;
+      s.v.store(found, std::memory_order_relaxed);
+      s.ctx_id.store(ctx, std::memory_order_release);
     }
-    *out = got;
+    *out = s.v.load(std::memory_order_relaxed);
     return cudaSuccess;
   }
 };
-// Opts a kernel into `bytes` of dynamic shared memory, once per device, and
+// Opts a kernel into `bytes` of dynamic shared memory, once per context, and
 // asks for the largest split of shared memory: an SM cannot take CTAs of a
 // kernel with another split before it has drained, which kept a short kernel
 // from starting beside the one before it (quantize and dequantize of 1001 x
@@ -399,12 +416,6 @@ bool pdl_enabled();
 
 // Records a message for svdq_last_error() and returns `status`.
 int record_error(int status, const char* fmt, ...);
-
-// Unique id (cuCtxGetId) of the calling thread's current CUDA context, or 0
-// when no context is current or the driver cannot tell.  Ids are never
-// reused within a process, so a device address cached under one id is
-// known to be stale once the id changes (for example after cudaDeviceReset).
-unsigned long long current_context_id();
 
 // Tensor-map encoding through the driver entry point (no libcuda link needed).
 bool encode_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,

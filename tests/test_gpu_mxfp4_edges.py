@@ -1,5 +1,8 @@
 """MXFP4 operators on the GPU where they could go wrong unnoticed: the ends of
-the range, waits beside a slow kernel."""
+the range, waits beside a slow kernel, a second driver context."""
+import os
+import subprocess
+import sys
 import time
 
 import numpy as np
@@ -13,6 +16,8 @@ from tests import mxfp4_cases as C
 from tests.helpers import nibbles
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def cuda(a, dtype=None):
@@ -106,3 +111,88 @@ def test_waiting_for_the_kernel_before_is_no_timeout():
             assert torch.equal(y, want)
     finally:
         B.set_timeout_ns(old)
+
+
+# ---------------------------------------------------------------- contexts --
+
+CONTEXTS = r"""
+import ctypes, os, sys
+import numpy as np
+sys.path.insert(0, sys.argv[1])
+import bit_w4a4_diffusion_b200 as B
+from oracle import mxfp4 as O
+from tests import mxfp4_cases as C
+
+cu = ctypes.CDLL("libcuda.so.1")
+def ok(e): assert e == 0, f"driver error {e}"
+def lib(e): assert e == 0, (e, B.lib.svdq_last_error())
+ok(cu.cuInit(0))
+held = []
+def put(a):
+    a = np.ascontiguousarray(a)
+    p = ctypes.c_uint64()
+    ok(cu.cuMemAlloc_v2(ctypes.byref(p), ctypes.c_size_t(a.nbytes)))
+    ok(cu.cuMemcpyHtoD_v2(p, a.ctypes.data_as(ctypes.c_void_p), ctypes.c_size_t(a.nbytes)))
+    held.append(p)
+    return p.value
+def get(p, shape, dtype):
+    a = np.empty(shape, dtype)
+    ok(cu.cuCtxSynchronize())
+    ok(cu.cuMemcpyDtoH_v2(a.ctypes.data_as(ctypes.c_void_p), ctypes.c_uint64(p), ctypes.c_size_t(a.nbytes)))
+    return a
+
+rng = np.random.default_rng(0)
+M, N, K = 300, 256, 320
+a, sa = C.operand(rng, M, K, -3)
+w, sw = C.operand(rng, N, K, -2)
+want = C.rounded(O.product(O.values(a, sa), O.values(w, sw)), C.torch.bfloat16).view(C.torch.int16).numpy()
+vals = O.values(a, sa).astype(np.float32)
+off = np.array([0, M], np.int32)
+
+def run():
+    '''Every kernel that asks for more shared memory than it gets by itself.'''
+    qa, qs, dw, ds, do = put(O.pack(a)), put(O.tile(sa, K)), put(O.pack(w)), put(O.tile(sw, K)), put(off)
+    y = put(np.zeros((M, N), np.int16))
+    for kernel in ("narrow", "pair256", "pair384"):
+        os.environ["SVDQ_MXFP4_GEMM_KERNEL"] = kernel
+        lib(B.lib.mxfp4_gemm(0, M, N, K, qa, qs, dw, ds, None, y, N, None, None))
+        assert np.array_equal(get(y, (M, N), np.int16), want), kernel
+    h = []
+    gs = put(np.zeros(B.mxfp4_scale_bytes(M, K, 1), np.uint8))
+    x, codes = put(vals), put(np.zeros((M, K // 2), np.uint8))
+    lib(B.lib.mxfp4_quantize(2, M, K, x, K, None, M, 1, do, codes, gs, None, None))
+    for kernel in ("narrow", "pair"):
+        os.environ["SVDQ_MXFP4_GEMM_KERNEL"] = kernel
+        hc, hs = put(np.zeros((M, N // 4), np.uint8)), put(np.zeros(B.mxfp4_scale_bytes(M, N // 2, 1), np.uint8))
+        lib(B.lib.mxfp4_grouped_gemm_swiglu_quant(0, 1, M, N // 2, K, do, codes, gs, dw, put(np.concatenate(
+            [O.tile(s, K) for s in (sw[:N // 2], sw[N // 2:])])), None, hc, hs, None, None))
+        h.append(get(hc, (M, N // 4), np.uint8))
+    assert np.array_equal(h[0], h[1]) and h[0].any()
+    del os.environ["SVDQ_MXFP4_GEMM_KERNEL"]
+    lib(B.lib.mxfp4_linear(0, 4, N, K, put((vals.view(np.uint32)[:4] >> 16).astype(np.uint16)), K, dw, ds, None, y, N,
+                           None, 0, None, None))
+    out = put(np.zeros((M, K), np.float32))
+    lib(B.lib.mxfp4_dequantize(2, M, K, qa, qs, 0, None, out, K, None, None))
+    assert np.array_equal(get(out, (M, K), np.float32), vals)
+
+dev = ctypes.c_int()
+ok(cu.cuDeviceGet(ctypes.byref(dev), 0))
+ctxs = []
+for _ in range(2):
+    c = ctypes.c_void_p()
+    ok(cu.cuCtxCreate_v2(ctypes.byref(c), 0, dev))
+    ctxs.append(c)
+for c in (ctxs[0], ctxs[1], ctxs[0]):
+    ok(cu.cuCtxSetCurrent(c))
+    run()
+for c in ctxs:
+    ok(cu.cuCtxDestroy_v2(c))
+print("contexts ok")
+"""
+
+
+def test_calls_in_two_driver_contexts():
+    """What a kernel was granted in one context of a device does not hold in
+    another (or after a reset): every call looks at the context it is in."""
+    r = subprocess.run([sys.executable, "-c", CONTEXTS, ROOT], capture_output=True, text=True, cwd=ROOT, timeout=300)
+    assert r.returncode == 0 and "contexts ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
