@@ -7,7 +7,7 @@ it checks dtypes / devices, allocates outputs with torch when the caller gives
 none, and passes raw pointers and the current CUDA stream to the library.  All arithmetic of the
 layer happens in the library's CUDA kernels (or, for the offline weight pack,
 in its C++ host code).  If the library is missing, importing this package
-raises: there is no fallback.
+raises, and if the module is, the MXFP4 calls do: there is no fallback.
 """
 import ctypes
 import os
@@ -91,9 +91,24 @@ def _load():
 
 lib = _load()
 
-from . import _mxfp4  # noqa: E402  (linked to the library that _load checks for)
 
-_mxfp4.set_error(SvdqError)
+class _Unavailable:
+    """Stands for the extension module where it cannot be imported: the MXFP4
+    calls raise then, and all others, which are plain ctypes, work."""
+
+    def __init__(self, reason):
+        self._reason = reason
+
+    def __getattr__(self, name):
+        raise ImportError(f"the MXFP4 calls need the extension module _mxfp4: {self._reason} "
+                          "(run `python bit_w4a4_diffusion_b200/build.py`)")
+
+
+try:
+    from . import _mxfp4  # noqa: E402  (linked to the library that _load checks for)
+    _mxfp4.set_error(SvdqError)
+except ImportError as e:
+    _mxfp4 = _Unavailable(e)
 
 
 def _check(status):
