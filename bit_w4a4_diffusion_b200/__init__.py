@@ -106,6 +106,8 @@ class _Unavailable:
 
 try:
     from . import _mxfp4  # noqa: E402  (linked to the library that _load checks for)
+    if _mxfp4.built_for_torch != str(torch.__version__):
+        raise ImportError(f"it was built for torch {_mxfp4.built_for_torch}, this is {torch.__version__}")
     _mxfp4.set_error(SvdqError)
 except ImportError as e:
     _mxfp4 = _Unavailable(e)

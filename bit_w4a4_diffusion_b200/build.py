@@ -8,6 +8,7 @@ newer than the object.  Cross-compiles without a GPU.
 """
 import importlib.util
 import os
+import runpy
 import subprocess
 import sys
 import sysconfig
@@ -18,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "lib", "libsvdq_b200.so")
-BIND = os.path.join(PKG, "_mxfp4.so")
+# Named for the interpreter it is built for, so that another one does not load it.
+BIND = os.path.join(PKG, "_mxfp4" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -84,17 +86,29 @@ def build(verbose=False, ptxas_verbose=False):
 
 
 def _build_bind(hdrs, verbose):
-    """The extension module, against the installed torch and the library."""
+    """The extension module, against the installed torch and the library.  It
+    is rebuilt when its command changes, which names the torch version: an
+    installed file's time need not be newer than the module."""
     src = os.path.join(CSRC, BIND_SOURCE)
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
-    if not _stale(BIND, [src, os.path.join(torch, "version.py")] + hdrs):
-        return
-    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+    version = runpy.run_path(os.path.join(torch, "version.py"))["__version__"]
+    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", f'-DBUILT_FOR_TORCH="{version}"',
+             "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
              "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
              "-I", "/usr/local/cuda/include"]
     libs = ["-L", os.path.dirname(LIB), "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"), "-ltorch_python",
             "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN/lib"]
-    _run(["g++"] + flags + [src, "-o", BIND] + libs, verbose)
+    cmd = ["g++"] + flags + [src, "-o", BIND] + libs
+    made_by = os.path.join(BUILD, BIND_SOURCE + ".cmd")
+    same = os.path.exists(made_by) and open(made_by).read() == "\n".join(cmd)
+    if same and not _stale(BIND, [src] + hdrs):
+        return
+    _run(cmd, verbose)
+    with open(made_by, "w") as f:
+        f.write("\n".join(cmd))
+    untagged = os.path.join(PKG, "_mxfp4.so")    # what earlier builds made; any interpreter would load it
+    if os.path.exists(untagged):
+        os.remove(untagged)
 
 
 if __name__ == "__main__":

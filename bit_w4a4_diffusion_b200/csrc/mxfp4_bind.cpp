@@ -485,5 +485,10 @@ PyMODINIT_FUNC PyInit__mxfp4() {
   } keys[] = {{&g_codes, "codes"}, {&g_scales, "scales"}, {&g_N, "N"}, {&g_K, "K"}, {&g_E, "E"}};
   for (auto& k : keys)
     if (!(*k.key = PyUnicode_InternFromString(k.name))) return nullptr;
-  return PyModule_Create(&g_module);
+  PyObject* const module = PyModule_Create(&g_module);
+  if (module && PyModule_AddStringConstant(module, "built_for_torch", BUILT_FOR_TORCH) != 0) {
+    Py_DECREF(module);
+    return nullptr;
+  }
+  return module;
 }

@@ -1,9 +1,11 @@
 """The package without its extension module, which is built against one torch
 and one Python: only the MXFP4 calls need it."""
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 import bit_w4a4_diffusion_b200 as B
 
@@ -46,3 +48,46 @@ def test_the_other_calls_need_no_extension_module(tmp_path):
 
 def test_a_module_that_does_not_load(tmp_path):
     use_package(tmp_path, "undefined symbol", _mxfp4="raise ImportError('undefined symbol')")
+
+
+def test_a_module_of_another_torch(tmp_path):
+    use_package(tmp_path, "built for torch 0.0.1", _mxfp4="built_for_torch = '0.0.1'\n"
+                "def set_error(e): pass\ndef quantize(*a): return 1\ndef linear(*a): return 1\n")
+
+
+def test_the_build_follows_the_installed_torch(tmp_path, monkeypatch):
+    """Another torch is another module, also where the installer keeps old
+    file times; the same one is built once."""
+    spec = importlib.util.spec_from_file_location("_build_under_test", os.path.join(PKG, "build.py"))
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    torch = tmp_path / "torch"
+    torch.mkdir()
+
+    def install(version):
+        (torch / "version.py").write_text(f"__version__ = {version!r}\n")
+        os.utime(torch / "version.py", (0, 0))
+
+    built = []
+
+    def run(cmd, verbose):
+        built.append(cmd)
+        with open(build.BIND, "w") as f:
+            f.write("module")
+
+    class Spec:
+        origin = str(torch / "__init__.py")
+
+    monkeypatch.setattr(build, "BIND", str(tmp_path / "_mxfp4.so"))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "PKG", str(tmp_path / "elsewhere"))
+    monkeypatch.setattr(build, "_run", run)
+    monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: Spec)
+    for version, count in (("9.9.0", 1), ("9.9.0", 1), ("9.9.1", 2), ("9.9.1", 2), ("9.9.0", 3)):
+        install(version)
+        build._build_bind([], False)
+        assert len(built) == count, (version, len(built))
+
+
+def test_the_module_is_named_for_its_interpreter():
+    assert os.path.basename(B._mxfp4.__file__).split(".", 1)[1] == sysconfig.get_config_var("EXT_SUFFIX")[1:]
