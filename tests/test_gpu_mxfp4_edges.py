@@ -1,5 +1,6 @@
 """MXFP4 operators on the GPU where they could go wrong unnoticed: the ends of
-the range, waits beside a slow kernel, a second driver context."""
+the range, waits beside a slow kernel, a second driver context; and what the
+smoke run reaches."""
 import os
 import subprocess
 import sys
@@ -196,3 +197,18 @@ def test_calls_in_two_driver_contexts():
     another (or after a reset): every call looks at the context it is in."""
     r = subprocess.run([sys.executable, "-c", CONTEXTS, ROOT], capture_output=True, text=True, cwd=ROOT, timeout=300)
     assert r.returncode == 0 and "contexts ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
+
+
+# ------------------------------------------------------------------- smoke --
+
+def test_smoke_reaches_every_mxfp4_product():
+    """The smoke run launches the narrow and the pair kernel of both products."""
+    import __graft_entry__ as entry
+    from torch.profiler import ProfilerActivity, profile
+    with profile(activities=[ProfilerActivity.CUDA]) as prof:
+        entry.smoke()
+        torch.cuda.synchronize()
+    names = " ".join(e.key for e in prof.key_averages())
+    for kernel in ("mxfp4_quantize_kernel", "mxfp4_gemm_narrow_kernel", "mxfp4_gemm_pair_kernel",
+                   "mxfp4_gemm_pair_swiglu_kernel"):
+        assert kernel in names, kernel
