@@ -55,11 +55,7 @@ struct MxRaw32 {
 // Eight consecutive elements of a row: how they are loaded, their largest
 // magnitude (NaN if there is one), two halves of a word for 16-bit types and
 // in the end as fp32 bits, and their fp32 values times a power of two.
-SVDQ_DEV uint4 mx_load_vec(const void* p, bool reused) {
-  const uint4* q = static_cast<const uint4*>(p);
-  return reused ? __ldg(q) : __ldcs(q);
-}
-// The same, issued where it stands: not moved behind a wait to its first use.
+// Issued where it stands: not moved behind a wait to its first use.
 SVDQ_DEV uint4 mx_load_now(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -86,7 +82,6 @@ struct MxElems<kMxBf16> {
   using Raw = MxRaw16;
   static constexpr int kSize = 2;
   static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0)}; }
-  static SVDQ_DEV Raw load(const uint8_t* x, bool reused) { return {mx_load_vec(x, reused)}; }
   static SVDQ_DEV Raw load_now(const uint8_t* x) { return {mx_load_now(x)}; }
   static SVDQ_DEV uint32_t top(const Raw& r) { return mx_top8<__nv_bfloat162>(r.w); }
   static SVDQ_DEV uint32_t top_max(uint32_t a, uint32_t b) { return mx_max2<__nv_bfloat162>(a, b); }
@@ -104,7 +99,6 @@ struct MxElems<kMxFp16> {
   using Raw = MxRaw16;
   static constexpr int kSize = 2;
   static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0)}; }
-  static SVDQ_DEV Raw load(const uint8_t* x, bool reused) { return {mx_load_vec(x, reused)}; }
   static SVDQ_DEV Raw load_now(const uint8_t* x) { return {mx_load_now(x)}; }
   static SVDQ_DEV uint32_t top(const Raw& r) { return mx_top8<__half2>(r.w); }
   static SVDQ_DEV uint32_t top_max(uint32_t a, uint32_t b) { return mx_max2<__half2>(a, b); }
@@ -123,9 +117,6 @@ struct MxElems<kMxFp32> {
   using Raw = MxRaw32;
   static constexpr int kSize = 4;
   static SVDQ_DEV Raw zero() { return {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
-  static SVDQ_DEV Raw load(const uint8_t* x, bool reused) {
-    return {mx_load_vec(x, reused), mx_load_vec(x + 16, reused)};
-  }
   static SVDQ_DEV uint32_t top(const Raw& r) {
     const uint32_t m = 0x7FFFFFFFu;
     return max(max(max(r.a.x & m, r.a.y & m), max(r.a.z & m, r.a.w & m)),

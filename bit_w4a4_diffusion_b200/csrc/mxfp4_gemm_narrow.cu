@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
         }
       };
       using Raw = typename E::Raw;
-      // The whole row index (at most 32 rows), loaded at the kernel's start.
+      // The whole row index (at most 16 rows, one a lane), loaded at the kernel's start.
       const int index = row_index;
       int count = 0, e = e0;   // slices of all tiles so far
       int filled = 0;
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
           // lies inside N or is padding of the last scale tile).
           const bool in_n = n0 + 32 * q < p.N;
           const int local = t.mt * ROWS + 32 * c;   // row within the group
-          const int nblk = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + local / 128;
+          const int nblk = mx_first_block(sched->off[t.e], t.e) + local / 128;   // SwiGLU is always grouped
           uint8_t* const sc = p.h_scales + mx_tile_offset(nblk, tiles_n, t.nt) + (local % 128) / 32 * 4 + q;
           uint8_t* const codes = p.h_codes + (size_t)(t.row0 + 32 * c) * (p.N / 2) + (n0 + 32 * q) / 2;
           // h goes through shared memory, so that a lane then holds a row's
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(num_threads<kGlu, kX>(), kMxNarrowPerSm)
                                 make_float2(0.f, 0.f)};
           const uint32_t code = sb == 255u ? 0u : mx_e2m1x8(v2);
           const int local = t.mt * ROWS + j;   // row within the group
-          const int block = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + local / 128;
+          const int block = mx_first_block(sched->off[t.e], t.e) + local / 128;
           if (in_n)
             *reinterpret_cast<uint16_t*>(p.h_codes + (size_t)(t.row0 + j) * (p.N / 2) + n / 2) = (uint16_t)code;
           if ((lane & 7) == 0)

@@ -100,9 +100,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc_pair(smem_u32(&ctl->tmem_base), TMEM_COLS);
     tmem_relinquish_pair();
   }
-  // Inputs may be of the preceding kernel's making, the offsets too; without
-  // groups all that comes before the loads goes before the wait.
-  if (p.groups != 0) pdl_wait();
+  // Inputs may be of the preceding kernel's making, the offsets too.
+  pdl_wait();
   if (warp == 0) mx_build_sched(&ctl->sched, p.groups, p.offsets, p.rows, 2 * BM, p.dev_status);
   // Both CTAs' barriers and tensor memory exist before either is used.
   __syncwarp();
@@ -112,12 +111,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem = ctl->tmem_base;
 
   const MxSched* const sched = &ctl->sched;
-  const int groups = p.groups == 0 ? 1 : p.groups;
+  const int groups = p.groups;   // at least one: the experts' products are always grouped
   const int k_slices = (p.K + 255) / 256, k_chunks = (p.K + 127) / 128;
   const int tiles_n = (p.N + BN_HALF - 1) / BN_HALF;         // = the 128-row scale blocks of one weight matrix
   const int num_tiles = sched->pre[groups] * tiles_n;
   const WaitCtx wctx{&ctl->abort_flag, p.dev_status, p.timeout_ns};
-  if (p.groups == 0) pdl_wait();
   pdl_launch_dependents();
 
   if (warp == PRODUCER_WARP) {
@@ -129,7 +127,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
       const MxTile t = mx_decode_tile(sched, groups, tile, tiles_n, 2 * BM, e);
       const int row0 = t.row0 + (int)rank * BM;
-      const int block_a = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + 2 * t.mt + (int)rank;
+      const int block_a = mx_first_block(sched->off[t.e], t.e) + 2 * t.mt + (int)rank;
       // The same 128 rows of the group's two matrices.
       const int row_w = (2 * t.e + (int)rank) * p.N + t.nt * BN_HALF;
       const int block_w0 = 2 * t.e * tiles_n + t.nt, block_w1 = block_w0 + tiles_n;
@@ -280,7 +278,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // r[0..1]: gate columns nw .. + 63, r[2..3]: the other factor's.  Each
       // 32-column half is one block of the next product's K.
       const int local = t.mt * 2 * BM + slab + lane;      // row within the group
-      const int block = (p.groups == 0 ? 0 : mx_first_block(sched->off[t.e], t.e)) + local / 128;
+      const int block = mx_first_block(sched->off[t.e], t.e) + local / 128;
       uint8_t* const sc = p.h_scales + mx_tile_offset(block, tiles_n, t.nt) + (local & 31) * 16 +
                           (local % 128) / 32 * 4 + 2 * h;
       uint8_t* const codes = p.h_codes + (size_t)(row0 + lane) * (p.N / 2) + nw / 2;
@@ -341,9 +339,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 cudaError_t launch_mxfp4_gemm_pair_swiglu(const MxGemmParams& p, const MxGemmTmaps& t, cudaStream_t stream,
                                           bool pdl) {
   if (cudaError_t e = mx_allow_smem<mxfp4_gemm_pair_swiglu_kernel>((int)kSmemBytes)) return e;
-  const long long by_rows = ((long long)p.rows + 2 * BM - 1) / (2 * BM);
-  const long long m_tiles =
-      p.groups == 0 ? by_rows : std::min<long long>(p.rows, p.rows / (2 * BM) + (long long)p.groups);
+  const long long m_tiles = std::min<long long>(p.rows, p.rows / (2 * BM) + (long long)p.groups);
   return mx_launch_pairs<mxfp4_gemm_pair_swiglu_kernel, NUM_THREADS, (int)kSmemBytes>(
       m_tiles * ((p.N + BN_HALF - 1) / BN_HALF), stream, pdl, t.act, t.w, t.sfa, t.sfw, p);
 }

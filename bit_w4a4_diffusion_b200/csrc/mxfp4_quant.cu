@@ -331,16 +331,12 @@ __global__ void __launch_bounds__(8 * 32) mxfp4_dequantize_kernel(const MxDequan
       b[t] = __ldg(p.scales + mx_tile_offset(block, k_chunks, chunk) + mx_row_offset(in_block) + (g & 3));
     }
   }
-  // Two staging buffers: while one unit's rows leave, the next is made.
-  const uint32_t base = smem_u32(staging) + (uint32_t)(warp * (spread ? 1 : 2) * kUnit);
+  // A staging buffer per unit: while one unit's rows leave, the next is made.
+  const uint32_t base = smem_u32(staging) + (uint32_t)(warp * (spread ? 1 : MQ_UNITS) * kUnit);
 #pragma unroll
   for (int t = 0; t < MQ_UNITS; ++t) {
     if (t >= units) break;
-    const uint32_t buf = base + (t & 1) * kUnit;
-    if (t >= 2) {
-      if (lane < 4) bulk_wait_read<1>();
-      __syncwarp();
-    }
+    const uint32_t buf = base + t * kUnit;
     // 2^(b - 127): b = 0 is the subnormal 2^-127, 255 is NaN.
     const float scale = __uint_as_float(b[t] == 255u ? 0x7FC00000u : b[t] == 0u ? 0x00400000u : b[t] << 23);
     const float2 scale2 = make_float2(scale, scale);
@@ -416,8 +412,8 @@ cudaError_t launch_quantize(const MxQuantParams& p, cudaStream_t stream, bool pd
 template <int kDtype>
 cudaError_t launch_dequantize(const MxDequantParams& p, cudaStream_t stream, bool pdl) {
   if (p.groups == 0)
-    return launch_rows<mxfp4_dequantize_kernel<kDtype, false>, 8, unit_bytes<kDtype>(), 2>(p, stream, pdl);
-  return launch_rows<mxfp4_dequantize_kernel<kDtype, true>, 8, unit_bytes<kDtype>(), 2>(p, stream, pdl);
+    return launch_rows<mxfp4_dequantize_kernel<kDtype, false>, 8, unit_bytes<kDtype>(), MQ_UNITS>(p, stream, pdl);
+  return launch_rows<mxfp4_dequantize_kernel<kDtype, true>, 8, unit_bytes<kDtype>(), MQ_UNITS>(p, stream, pdl);
 }
 
 }  // namespace
