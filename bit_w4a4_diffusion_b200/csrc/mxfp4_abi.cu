@@ -131,12 +131,7 @@ int quantize(const Device& d, int dtype, int rows, int K, const void* x, long lo
 // the host does not know: up to 16 rows are rarely many of one group.
 bool fuses(int groups, int rows) { return rows <= (groups == 0 ? MXFP4_FUSED_ROWS : MXFP4_FUSED_GROUPED_ROWS); }
 
-// Row tiles of the narrow kernel: every group's last tile may be short, and a
-// tile has a row.
-long long narrow_m_tiles(int groups, int rows) {
-  return groups == 0 ? ((long long)rows + kMxNarrowRows - 1) / kMxNarrowRows
-                     : std::min<long long>(rows, rows / kMxNarrowRows + (long long)groups);
-}
+long long narrow_m_tiles(int groups, int rows) { return mx_row_tiles(groups, rows, kMxNarrowRows); }
 
 // SVDQ_MXFP4_GEMM_KERNEL (read at every call) forces a kernel: "narrow",
 // "pair", or "pair256" / "pair384" for the pair kernel with tiles of that width.

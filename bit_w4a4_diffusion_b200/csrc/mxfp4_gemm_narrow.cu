@@ -658,10 +658,7 @@ cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, int num_sms
   auto kernel = mxfp4_gemm_narrow_kernel<kGlu, kX>;
   constexpr int smem = smem_bytes<kGlu, kX>();
   if (cudaError_t e = mx_allow_smem<mxfp4_gemm_narrow_kernel<kGlu, kX>>(smem)) return e;
-  // As many tiles as the rows can make: every group's last tile may be short.
-  const long long groups = p.groups == 0 ? 1 : p.groups;
-  const long long by_rows = (long long)(p.rows + ROWS - 1) / ROWS;
-  const long long m_tiles = p.groups == 0 ? by_rows : std::min<long long>(p.rows, p.rows / ROWS + groups);
+  const long long m_tiles = mx_row_tiles(p.groups, p.rows, ROWS);
   const long long tiles = m_tiles * ((p.N + BW - 1) / BW);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.splits > 1 ? tiles * p.splits

@@ -370,9 +370,7 @@ template <int kParts>
 cudaError_t launch_impl(const MxGemmParams& p, const MxGemmTmaps& t, cudaStream_t stream, bool pdl) {
   constexpr int kSmem = smem_bytes<kParts>(), kCols = Cfg<kParts>::kCols;
   if (cudaError_t e = mx_allow_smem<mxfp4_gemm_pair_kernel<kParts>>(kSmem)) return e;
-  const long long m_tiles = p.groups == 0
-                                ? ((long long)p.rows + 2 * BM - 1) / (2 * BM)
-                                : std::min<long long>(p.rows, p.rows / (2 * BM) + (long long)p.groups);
+  const long long m_tiles = mx_row_tiles(p.groups, p.rows, 2 * BM);
   return mx_launch_pairs<mxfp4_gemm_pair_kernel<kParts>, NUM_THREADS, kSmem>(
       m_tiles * ((p.N + kCols - 1) / kCols), stream, pdl, t.act, t.w, t.sfa, t.sfw, t.y, p);
 }

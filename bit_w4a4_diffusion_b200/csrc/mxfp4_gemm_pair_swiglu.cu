@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 cudaError_t launch_mxfp4_gemm_pair_swiglu(const MxGemmParams& p, const MxGemmTmaps& t, cudaStream_t stream,
                                           bool pdl) {
   if (cudaError_t e = mx_allow_smem<mxfp4_gemm_pair_swiglu_kernel>((int)kSmemBytes)) return e;
-  const long long m_tiles = std::min<long long>(p.rows, p.rows / (2 * BM) + (long long)p.groups);
+  const long long m_tiles = mx_row_tiles(p.groups, p.rows, 2 * BM);
   return mx_launch_pairs<mxfp4_gemm_pair_swiglu_kernel, NUM_THREADS, (int)kSmemBytes>(
       m_tiles * ((p.N + BN_HALF - 1) / BN_HALF), stream, pdl, t.act, t.w, t.sfa, t.sfw, p);
 }

@@ -322,6 +322,13 @@ constexpr int kMxFusedRows = 16;    // most rows of a product that quantizes x i
 cudaError_t launch_mxfp4_gemm_narrow(const MxGemmParams& p, const MxGemmTmaps& t, bool swiglu, int num_sms,
                                      cudaStream_t stream, bool pdl);
 
+// Row tiles of a product, at most (exact without groups): every group's last
+// tile may be short, and a tile has a row.
+inline long long mx_row_tiles(int groups, int rows, int tile_rows) {
+  return groups == 0 ? ((long long)rows + tile_rows - 1) / tile_rows
+                     : std::min<long long>(rows, rows / tile_rows + (long long)groups);
+}
+
 // Unique id (cuCtxGetId) of the calling thread's current CUDA context, or 0
 // when no context is current or the driver cannot tell.  Ids are never
 // reused within a process, so what was found under one id (a device address,
