@@ -199,6 +199,111 @@ def test_calls_in_two_driver_contexts():
     assert r.returncode == 0 and "contexts ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
 
 
+# ------------------------------------------------------- codes and padding --
+
+@pytest.mark.parametrize("kernel", ["pair256", "pair384", "narrow"])
+def test_every_code_pair_at_every_place(monkeypatch, kernel):
+    """One-element rows: at each of the 256 places of a K slice all 256 pairs
+    of E2M1 codes, scales over a wide range.  Row n of the weight and row n of
+    the activations have their element at k = n; others meet in no place."""
+    monkeypatch.setenv("SVDQ_MXFP4_GEMM_KERNEL", kernel)
+    K, at = 256, np.arange(256)
+    rng = np.random.default_rng(0)
+    sa, sw = ((127 + rng.integers(-40, 41, (256, 8))).astype(np.uint8) for _ in range(2))
+    da, dw = cuda(O.tile(sa, K)), cuda(O.tile(sw, K))
+    scale = np.ldexp(1.0, sa[at, at // 32].astype(np.int64) + sw[at, at // 32] - 254)
+    got, want = [], []
+    for shift in range(256):
+        pair = (at + shift) % 256
+        a, w = np.zeros((2, 256, K), np.uint8)
+        a[at, at], w[at, at] = pair % 16, pair // 16
+        y = B.mxfp4_gemm(cuda(O.pack(a)), da, {"codes": cuda(O.pack(w)), "scales": dw, "N": 256, "K": K})
+        got.append(y)
+        want.append(np.diag(F.E2M1_VALUE[pair % 16] * F.E2M1_VALUE[pair // 16] * scale))
+    got = torch.stack(got).double().cpu()              # at most 6 significant bits: exact in bf16
+    assert torch.equal(got, torch.from_numpy(np.stack(want)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(1, 32), (5, 96), (33, 160), (128, 1056), (129, 320), (300, 2080)])
+def test_quantizer_writes_zero_padding(M, K, dtype):
+    """Scale bytes of the blocks past K are 0 in every real row, whatever the
+    buffer held, of a whole matrix and of row groups."""
+    x = C.rows(np.random.default_rng(M), M, K, dtype).cuda()
+    codes = torch.empty(M, K // 2, dtype=torch.uint8, device="cuda")
+    want = O.quantize(x.double().cpu().numpy())[1]
+    padded = -(-K // 128) * 4
+    r, g = np.meshgrid(np.arange(M), np.arange(padded), indexing="ij")
+    full = np.zeros((M, padded), np.uint8)
+    full[:, :K // 32] = want
+    scales = torch.full((B.mxfp4_scale_bytes(M, K),), 0xFF, dtype=torch.uint8, device="cuda")
+    B.mxfp4_quantize(x, out=(codes, scales))
+    assert np.array_equal(scales.cpu().numpy()[O.scale_place(r, g, K)], full)
+    off = [0, 0, M // 3, M // 2, M]
+    scales = torch.full((B.mxfp4_scale_bytes(M, K, 4),), 0xFF, dtype=torch.uint8, device="cuda")
+    B.mxfp4_quantize(x, offsets=cuda(off, torch.int32), out=(codes, scales))
+    got = scales.cpu().numpy()
+    for e in range(4):
+        rows = r[:off[e + 1] - off[e]]
+        at = (off[e] // 128 + e) * (padded // 4) * 512 + O.scale_place(rows, g[:len(rows)], K)
+        assert np.array_equal(got[at], full[off[e]:off[e + 1]])
+
+
+def test_wrong_tensors_are_refused():
+    """Types, devices and sizes of CUDA tensors, one wrong at a time."""
+    x = torch.zeros(20, 64, dtype=torch.bfloat16, device="cuda")
+    off = cuda([0, 12, 20], torch.int32)
+    w = random_weight((2,), 32, 64)
+    up = random_weight((2, 2), 32, 64)
+    down = random_weight((2,), 64, 32)
+    one = {**w, "codes": w["codes"][0], "scales": w["scales"][0], "E": 1}
+    codes, scales = B.mxfp4_quantize(x)
+    index = torch.zeros(20, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def calls(x=x, off=off, w=w, up=up, down=down, one=one, codes=codes, scales=scales, index=index, status=status):
+        return [lambda: B.mxfp4_quantize(x, offsets=off, row_index=index, dev_status=status),
+                lambda: B.mxfp4_dequantize(codes, scales, dev_status=status),
+                lambda: B.mxfp4_gemm(codes, scales, one, dev_status=status),
+                lambda: B.mxfp4_linear(x, one, dev_status=status),
+                lambda: B.mxfp4_grouped_linear(x, off, w, row_index=index, dev_status=status),
+                lambda: B.mxfp4_grouped_mlp_swiglu(x, off, up, down, row_index=index, dev_status=status)]
+
+    for call in calls():
+        call()
+    quantize, dequantize, gemm, linear, grouped, mlp = range(6)
+    as_int8 = lambda t: {**t, "codes": t["codes"].view(torch.int8)}       # noqa: E731
+    on_host = lambda t: {**t, "scales": t["scales"].cpu()}                # noqa: E731
+    short = lambda t: {**t, "scales": t["scales"].reshape(-1)[:-1]}       # noqa: E731
+    wider = lambda t: {**t, "N": t["N"] + 8}                              # noqa: E731
+    for kw, which, error in [
+            (dict(x=x.double()), (quantize, linear, grouped, mlp), TypeError),
+            (dict(x=x.float()), (linear, grouped, mlp), TypeError),
+            (dict(x=x.cpu()), (quantize, linear, grouped, mlp), TypeError),
+            (dict(x=x[0]), (quantize, linear, grouped, mlp), TypeError),
+            (dict(off=off.long()), (quantize, grouped, mlp), TypeError),
+            (dict(off=off.cpu()), (quantize, grouped, mlp), TypeError),
+            (dict(off=off[:1]), (quantize, grouped, mlp), TypeError),
+            (dict(index=index.long()), (quantize, grouped, mlp), TypeError),
+            (dict(index=index.cpu()), (quantize, grouped, mlp), TypeError),
+            (dict(codes=codes.view(torch.int8)), (dequantize, gemm), TypeError),
+            (dict(scales=scales.view(torch.int8)), (dequantize, gemm), TypeError),
+            (dict(scales=scales[:-1]), (dequantize, gemm), ValueError),
+            (dict(one=as_int8(one), w=as_int8(w), up=as_int8(up)), (gemm, linear, grouped, mlp), TypeError),
+            (dict(one=on_host(one), w=on_host(w), down=on_host(down)), (gemm, linear, grouped, mlp), TypeError),
+            (dict(one=short(one), w=short(w), down=short(down)), (gemm, linear, grouped, mlp), ValueError),
+            (dict(one=wider(one), w=wider(w), up=wider(up)), (gemm, linear, grouped, mlp), ValueError),
+            (dict(w={**w, "E": 3}, up={**up, "E": 2}), (grouped, mlp), B.SvdqError),
+            (dict(status=status.float()), range(6), TypeError),
+            (dict(status=status.cpu()), range(6), TypeError)]:
+        for i in which:
+            with pytest.raises(error):
+                calls(**kw)[i]()
+    for call in calls():
+        call()
+    assert int(status) == 0
+
+
 # ------------------------------------------------------------------- smoke --
 
 def test_smoke_reaches_every_mxfp4_product():
