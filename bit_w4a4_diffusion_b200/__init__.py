@@ -544,7 +544,11 @@ def _mx_elsewhere(t, stream):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("a CUDA tensor is expected")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=t.device)
+        handle = _stream(stream)
+        # The default stream's handles, 0 and 1, are not external ones: an
+        # ExternalStream(0) is a new stream.
+        stream = (torch.cuda.default_stream(t.device) if handle in (0, 1) else
+                  torch.cuda.ExternalStream(handle, device=t.device))
     if stream.device != t.device:
         raise ValueError(f"the stream is of {stream.device}, the tensors of {t.device}")
     return torch.cuda.stream(stream)

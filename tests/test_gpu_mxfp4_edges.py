@@ -199,6 +199,33 @@ def test_calls_in_two_driver_contexts():
     assert r.returncode == 0 and "contexts ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
 
 
+# ------------------------------------------------------------ stream handles --
+
+@pytest.mark.parametrize("handle", [0, 1, None])
+def test_the_default_stream_by_its_handle(handle):
+    """stream=0, which is what torch.cuda.current_stream().cuda_stream mostly is
+    (or 1, the default stream's other handle): behind the work that is queued
+    there, before the work that follows."""
+    if handle is None:
+        handle = torch.cuda.current_stream().cuda_stream
+        assert handle == 0
+    rng = np.random.default_rng(3)
+    w = random_weight((), 264, 320)
+    xs = [C.rows(rng, 40, 320, torch.bfloat16).cuda() for _ in range(2)]
+    want = [B.mxfp4_linear(x, w) for x in xs]
+    x, y = torch.empty_like(xs[0]), torch.empty_like(want[0])
+    busy = torch.randn(4096, 4096, device="cuda")
+    got = []
+    for i in range(6):
+        torch.mm(busy, busy)                          # the copy waits for it
+        x.copy_(xs[i % 2])
+        assert B.mxfp4_linear(x, w, y=y, stream=handle) is y
+        got.append(y.clone())
+        got.append(B.mxfp4_linear(x, w, stream=handle).clone())
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i // 2 % 2]), i
+
+
 # ------------------------------------------------------- codes and padding --
 
 @pytest.mark.parametrize("kernel", ["pair256", "pair384", "narrow"])
