@@ -627,7 +627,9 @@ def mxfp4_grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index=None, up_bias=N
                              workspace=None, dev_status=None, stream=None):
     """The experts' MLP y = down(SwiGLU(up(x))) per row group: w_up two
     matrices [I, K] per group (gate, other), w_down [groups, K, I]; the hidden
-    rows are quantized in the up product's epilogue."""
+    rows are quantized in the up product's epilogue.  SwiGLU is g sigmoid(g) u,
+    without clamps or offsets; for other activations use two
+    mxfp4_grouped_linear calls."""
     if stream is None:
         return _mxfp4.grouped_mlp_swiglu(x, offsets, w_up, w_down, row_index, up_bias, down_bias, y, workspace,
                                          dev_status)

@@ -148,6 +148,11 @@ bool forced(const char* name, size_t n) {
 //   32 groups, 2048 x 2048, rows each: 96 21.0 / 22.4, 128 21.8 / 23.5, 160 27.5 / 23.9
 //   SwiGLU, the same: 64 27.0 / 33.6, 96 34.7 / 33.8, 160 43.8 / 34.3
 //   MLP, 32 uneven groups, 2048 x 1024: 75 rows 36.5 / 40.2, 125 46.5 / 42.9 (up product)
+// The average stands for the groups, whose sizes the host does not know.  With
+// most rows in one of 32 groups, 2048 x 2048, narrow / pair (* chosen), its
+// share of the rows:
+//   4096 rows: 30% 24.3* / 21.4, 60% 23.8* / 28.3, 90% 27.1* / 25.9;  8192 rows: 90% 41.7 / 35.8*
+//   SwiGLU, 4096: 30% 41.1 / 42.5*, 60% 41.4 / 47.3*, 90% 44.8 / 47.0*;  8192: 90% 72.8 / 61.0*
 bool use_pair(int groups, int rows, int N, bool swiglu, int sms) {
   if (forced("pair", 4)) return true;
   if (forced("narrow", 6)) return false;

@@ -430,8 +430,9 @@ int awq_w4a16_linear(int M, int N, int K, const void* x, const void* qweight, co
  * 128-row block offsets[e]/128 + e and are numbered from 0 there.
  * Offsets that decrease or leave [0, rows], and row indices outside
  * [0, x_rows), are reported as code 5 through dev_status / svdq_device_status;
- * the products of such a call write nothing, a row with a bad index becomes
- * NaN.  Outputs and workspace must not overlap an input or each other.
+ * the products of a call with bad offsets write nothing (the quantizer and
+ * its inverse still write rows whose own group lies in order), a row with a
+ * bad index becomes NaN.  Outputs and workspace must not overlap an input or each other.
  *
  * All entry points: K % 32 == 0, N % 8 == 0, rows from 0 (nothing is done)
  * to 2^30, groups 1 to 512.  dtype is the type of x, y and bias; the row
@@ -507,7 +508,9 @@ int mxfp4_grouped_linear(int dtype, int groups, int rows, int N, int K, const vo
  * leaves the chip.  Each group has two weights [I, K], the gate's and the
  * other factor's (w_codes [groups, 2, I, K/2], scales per matrix, bias
  * [groups, 2, I] or NULL, of type dtype):
- *   g, u = the two products + bias (fp32);  h = g sigmoid(g) u;
+ *   g, u = the two products + bias (fp32);  h = g sigmoid(g) u (no clamp,
+ *   scale or offset of either factor: other activations take the grouped
+ *   linear calls with the caller's own between them);
  *   h_codes [rows, I/2], h_scales (grouped layout, K = I) = Q(h).
  * I % 32 == 0.
  * mxfp4_grouped_mlp_swiglu: y = down(Q(h)), h from Q(x): mxfp4_quantize, the
