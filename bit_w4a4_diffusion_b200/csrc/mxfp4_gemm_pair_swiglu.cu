@@ -8,7 +8,7 @@
 // What bounds it: mostly the operands' way from L2 to shared memory, about 84
 // GB/s per SM with every SM loading; a 256-column K slice of a tile is 35 KB
 // per SM (rows 16 KB, 128 weight rows 16 KB, scales 3 KB) for 256 x 256 x 256
-// multiply-adds on two SMs, which keeps the tensor pipe active 65% of the time.
+// multiply-adds on two SMs, which keeps the tensor pipe active 63% of the time.
 // After that the epilogue: without the exponential and the quotient 16 x 1024
 // rows, 2048 of 4096, take 101.5 us instead of 107.7, 64 x 512 rows, 1024 of
 // 2048, 61 instead of 66.  The rows are the M operand, so that a thread holds a
