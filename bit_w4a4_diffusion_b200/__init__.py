@@ -10,6 +10,7 @@ in its C++ host code).  If the library is missing, importing this package
 raises, and if the module is, the MXFP4 calls do: there is no fallback.
 """
 import ctypes
+import importlib
 import os
 
 import numpy as np
@@ -105,7 +106,8 @@ class _Unavailable:
 
 
 try:
-    from . import _mxfp4  # noqa: E402  (linked to the library that _load checks for)
+    # (Not `from . import`, which after a reload gives what this name was before.)
+    _mxfp4 = importlib.import_module("._mxfp4", __name__)   # linked to the library that _load checks for
     if _mxfp4.built_for_torch != str(torch.__version__):
         raise ImportError(f"it was built for torch {_mxfp4.built_for_torch}, this is {torch.__version__}")
     _mxfp4.set_error(SvdqError)

@@ -7,6 +7,8 @@ import subprocess
 import sys
 import sysconfig
 
+import pytest
+
 import bit_w4a4_diffusion_b200 as B
 
 PKG = os.path.dirname(os.path.abspath(B.__file__))
@@ -28,8 +30,9 @@ print("fine")
 """
 
 
-def use_package(tmp_path, why, **files):
-    """Imports a copy of the package with `files` in place of the module."""
+def run_in_copy(tmp_path, program, **files):
+    """Runs a program beside a copy of the package with `files` in place of
+    the module."""
     pkg = tmp_path / "bit_w4a4_diffusion_b200"
     pkg.mkdir()
     shutil.copy(os.path.join(PKG, "__init__.py"), pkg)
@@ -37,9 +40,13 @@ def use_package(tmp_path, why, **files):
     for name, text in files.items():
         (pkg / (name + ".py")).write_text(text)
     env = {k: v for k, v in os.environ.items() if k != "PYTHONPATH"}
-    r = subprocess.run([sys.executable, "-c", USE.format(root=str(tmp_path), why=why)], cwd=tmp_path, env=env,
-                       capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", program], cwd=tmp_path, env=env, capture_output=True, text=True,
+                       timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def use_package(tmp_path, why, **files):
+    run_in_copy(tmp_path, USE.format(root=str(tmp_path), why=why), **files)
 
 
 def test_the_other_calls_need_no_extension_module(tmp_path):
@@ -91,3 +98,42 @@ def test_the_build_follows_the_installed_torch(tmp_path, monkeypatch):
 
 def test_the_module_is_named_for_its_interpreter():
     assert os.path.basename(B._mxfp4.__file__).split(".", 1)[1] == sysconfig.get_config_var("EXT_SUFFIX")[1:]
+
+
+RELOAD = """
+import importlib, os, torch
+import bit_w4a4_diffusion_b200 as B
+try:
+    B._mxfp4.quantize
+    raise AssertionError("there is no module yet")
+except ImportError:
+    pass
+with open(os.path.join(os.path.dirname(B.__file__), "_mxfp4.py"), "w") as f:
+    f.write(f"built_for_torch = {str(torch.__version__)!r}\\ndef set_error(e): pass\\ndef quantize(*a): return 7\\n")
+importlib.invalidate_caches()
+importlib.reload(B)
+assert B.mxfp4_quantize(torch.zeros(4, 64)) == 7
+print("fine")
+"""
+
+
+def test_a_module_built_later_is_found_by_a_reload(tmp_path):
+    run_in_copy(tmp_path, RELOAD)
+
+
+def test_build_entry_needs_the_module(monkeypatch):
+    """The package imports without its module; a build that left none is no
+    build."""
+    import __graft_entry__ as entry
+
+    class Nothing:
+        @staticmethod
+        def build(verbose):
+            pass
+
+    monkeypatch.setattr(entry, "_build_module", lambda: Nothing)
+    monkeypatch.setattr(entry.importlib, "reload", lambda module: module)
+    entry.build()
+    monkeypatch.setattr(B, "_mxfp4", B._Unavailable("left out"))
+    with pytest.raises(ImportError):
+        entry.build()
