@@ -432,7 +432,8 @@ int awq_w4a16_linear(int M, int N, int K, const void* x, const void* qweight, co
  * [0, x_rows), are reported as code 5 through dev_status / svdq_device_status;
  * the products of a call with bad offsets write nothing (the quantizer and
  * its inverse still write rows whose own group lies in order), a row with a
- * bad index becomes NaN.  Outputs and workspace must not overlap an input or each other.
+ * bad index becomes NaN.  Outputs and workspace must not overlap an input or
+ * each other.
  *
  * All entry points: K % 32 == 0, N % 8 == 0, rows from 0 (nothing is done)
  * to 2^30, groups 1 to 512.  dtype is the type of x, y and bias; the row
