@@ -108,8 +108,9 @@ class _Unavailable:
 try:
     # (Not `from . import`, which after a reload gives what this name was before.)
     _mxfp4 = importlib.import_module("._mxfp4", __name__)   # linked to the library that _load checks for
-    if _mxfp4.built_for_torch != str(torch.__version__):
-        raise ImportError(f"it was built for torch {_mxfp4.built_for_torch}, this is {torch.__version__}")
+    _built_for = getattr(_mxfp4, "built_for_torch", "of an earlier build")
+    if _built_for != str(torch.__version__):
+        raise ImportError(f"it was built for torch {_built_for}, this is {torch.__version__}")
     _mxfp4.set_error(SvdqError)
 except ImportError as e:
     _mxfp4 = _Unavailable(e)

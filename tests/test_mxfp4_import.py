@@ -62,6 +62,12 @@ def test_a_module_of_another_torch(tmp_path):
                 "def set_error(e): pass\ndef quantize(*a): return 1\ndef linear(*a): return 1\n")
 
 
+def test_a_module_that_does_not_say_what_it_was_built_for(tmp_path):
+    """One of an earlier build."""
+    use_package(tmp_path, "built for torch", _mxfp4="def set_error(e): pass\ndef quantize(*a): return 1\n"
+                "def linear(*a): return 1\n")
+
+
 def test_the_build_follows_the_installed_torch(tmp_path, monkeypatch):
     """Another torch is another module, also where the installer keeps old
     file times; the same one is built once."""
